@@ -18,6 +18,15 @@
  *   pbs_block_mass, pbs_coverage  diagnostics: attention coverage and
  *                      block-level density
  *
+ * and what stands before and behind the prefill in a decoding loop:
+ *
+ *   pbs_rope           rotary positions of Q and K, and their gradient
+ *   pbs_cache_*        a paged K/V cache whose page table lives on the
+ *                      device: reserve (copy-on-write), append, copy, fork,
+ *                      trim, compact, accept
+ *   pbs_tree_mask, pbs_tree_attn  attention of a tree of drafted tokens
+ *                      (one token: a decoding step) over that cache
+ *
  * Conventions shared by every call
  * --------------------------------
  * - Tensors are dense, row-major, head dim innermost, in DEVICE memory:
@@ -75,7 +84,8 @@ typedef enum {
   PBS_ERR_CUDA = 3,          /* a CUDA runtime call failed */
   PBS_ERR_TIMEOUT = 4,       /* a kernel's bounded wait ran out */
   PBS_ERR_DEVICE_ASSERT = 5, /* a kernel found an index out of range */
-  PBS_ERR_WORKSPACE = 6      /* workspace smaller than pbs_workspace_bytes */
+  PBS_ERR_WORKSPACE = 6,     /* workspace smaller than pbs_workspace_bytes */
+  PBS_ERR_PAGES = 7          /* a cache's pool has too few free pages */
 } pbs_status;
 
 typedef enum {
@@ -412,6 +422,189 @@ pbs_status pbs_block_mass(const void *q, const void *k_perm, const int32_t *kpos
 pbs_status pbs_coverage(const float *mass, const int32_t *blk_idx,
                         const int32_t *blk_cnt, double target, float *coverage,
                         int32_t *blocks_needed, pbs_shape s, pbs_stream_t st);
+
+/*
+ * Decoding: rotary positions, a paged K/V cache, trees of drafted tokens
+ * ---------------------------------------------------------------------
+ * These calls take strided rows: the head dimension is contiguous, every
+ * other stride is given in elements and is a multiple of 16 bytes, and the
+ * base pointer is 16-byte aligned. Like the prefill steps they only enqueue
+ * work on the stream, so they can be captured into a CUDA graph; what the
+ * device holds (lengths, tables, page counts) is read at replay time.
+ */
+typedef struct {
+  void *p;                           /* 16-byte aligned */
+  int64_t layer, batch, head, row;   /* strides in elements */
+} pbs_rows;
+
+typedef enum { PBS_BF16 = 0, PBS_FP16 = 1, PBS_FP32 = 2 } pbs_dtype;
+
+/*
+ * pbs_rope - rotary position embedding of Q and K in one launch.
+ *
+ * The first `rot` elements of each head are rot/2 pairs; pair i of a row at
+ * position t turns by the angle a = t * inv_freq[i]:
+ *     y0 = gain * (x0 cos a - x1 sin a)
+ *     y1 = gain * (x1 cos a + x0 sin a)
+ * with `transpose` by -a instead, which is the transposed map: the gradient
+ * of x from the gradient of y. Elements from `rot` on are copied.
+ * Layout 0 ("half"): pair i is (x[i], x[i + rot/2]); layout 1 ("pairs"):
+ * (x[2i], x[2i + 1]). The angle is reduced exactly (64-bit fixed-point
+ * turns), so it stays right at any int32 position; sums are fp32 and each
+ * element is rounded once.
+ *
+ *   q, q_out  [batch, hq, n, d]  (layer stride unused); y may be x itself
+ *   k, k_out  [batch, hkv, n, d] or k.p == NULL with hkv == 0
+ *   pos       int32, pos[b * pos_batch + i] (pos_batch 0: one row for all)
+ *   inv_freq  [rot/2] fp64, radians per position
+ * d and rot are multiples of 16, 0 <= rot <= d <= 1024.
+ */
+pbs_status pbs_rope(pbs_rows q, pbs_rows q_out, int hq, pbs_rows k, pbs_rows k_out, int hkv,
+                    const int32_t *pos, int64_t pos_batch, const double *inv_freq, float gain,
+                    int batch, int n, int d, int rot, int layout, int transpose, int dtype,
+                    pbs_stream_t st);
+
+/*
+ * A paged cache. Two pools, K and V, each [layers, pages, hkv, page, d] of
+ * 16-bit elements, dense. Row s of `table` [seqs, width] lists the pages of
+ * sequence s in order (token t lies in page table[s][t / page], row t %
+ * page), -1 where it holds none; `lens` [seqs] counts its tokens; `refs`
+ * [pages] counts the table entries that hold a page, 0 for a free one. One
+ * page index stands for that page of every layer. All three arrays are
+ * int32 in device memory. An index that points outside (a bad page, a
+ * sequence that does not exist) is recorded as PBS_ERR_DEVICE_ASSERT in
+ * the device error word and skipped; it never reads or writes out of range.
+ */
+typedef struct {
+  int layers, pages, hkv;
+  int page; /* tokens per page */
+  int d;    /* a multiple of 8; 64 or 128 for pbs_tree_attn */
+  int seqs, width;
+} pbs_cache;
+
+typedef enum {
+  PBS_CACHE_RESERVE = 0,
+  PBS_CACHE_COPY = 1,
+  PBS_CACHE_COMPACT = 2
+} pbs_cache_op;
+
+/* Bytes of device workspace a cache call needs (0 if none); `n`: the pairs
+ * of pbs_cache_copy. */
+size_t pbs_cache_workspace_bytes(pbs_cache c, int op, int n);
+
+/*
+ * pbs_cache_reserve - pages for the tokens lens[s] .. want[s]-1 of every
+ * sequence (none where want[s] <= lens[s]), each held by that sequence
+ * alone: a missing page is taken from the free ones, and a page that
+ * another sequence still holds is replaced (of k sequences that share it
+ * and write, the last one keeps it when nobody else holds it). Free pages
+ * are handed out lowest index first, in (sequence, position) order.
+ * copy_src[s], copy_dst[s]: the page pair to copy (pbs_cache_copy) because
+ * tokens below lens[s] lie in the replaced page; -1, -1 otherwise. lens is
+ * not changed. With too few free pages nothing changes, every pair is -1
+ * and the device error word becomes PBS_ERR_PAGES. A sequence with want
+ * beyond width * page, or a negative length, is reported and left alone.
+ */
+pbs_status pbs_cache_reserve(int32_t *table, int32_t *refs, const int32_t *lens,
+                             const int32_t *want, int32_t *copy_src, int32_t *copy_dst,
+                             pbs_cache c, void *ws, size_t ws_bytes, pbs_stream_t st);
+
+/*
+ * pbs_cache_append - rows i < count[s] (all n when count is NULL) of k, v
+ * [layers, seqs, hkv, n, d] written at tokens start[s] + i. The pages must
+ * be reserved. No other row of the pools is touched.
+ */
+pbs_status pbs_cache_append(pbs_rows k, pbs_rows v, int n, void *k_pages, void *v_pages,
+                            const int32_t *table, const int32_t *start, const int32_t *count,
+                            pbs_cache c, pbs_stream_t st);
+
+/*
+ * pbs_cache_copy - page src[i] copied to page dst[i] in both pools and every
+ * layer, i < n; a pair of -1 is skipped. The pairs happen at once, so a
+ * destination that an earlier pair has already, and a source that is some
+ * pair's destination, are reported and their pair skipped.
+ */
+pbs_status pbs_cache_copy(void *k_pages, void *v_pages, const int32_t *src, const int32_t *dst,
+                          int n, pbs_cache c, void *ws, size_t ws_bytes, pbs_stream_t st);
+
+/*
+ * pbs_cache_fork - sequence dst[i] becomes a second holder of sequence
+ * src[i]'s pages and gets its length, i < n; no page is copied until one of
+ * them writes (pbs_cache_reserve). A pair of -1 is skipped. dst[i] must be
+ * empty (no tokens, no pages), appear once, and be no pair's source.
+ */
+pbs_status pbs_cache_fork(int32_t *table, int32_t *refs, int32_t *lens, const int32_t *src,
+                          const int32_t *dst, int n, pbs_cache c, pbs_stream_t st);
+
+/*
+ * pbs_cache_trim - sequence s keeps its first min(lens[s], keep[s]) tokens;
+ * the pages behind them, reserved ones too, are released (freed where
+ * nobody else holds them). keep[s] == 0 frees the sequence, keep[s] < 0
+ * leaves it as it is.
+ */
+pbs_status pbs_cache_trim(int32_t *table, int32_t *refs, int32_t *lens, const int32_t *keep,
+                          pbs_cache c, pbs_stream_t st);
+
+/*
+ * pbs_cache_compact - the held pages moved to the low end of the pools: with
+ * n pages held, the k-th held page at or above n (in ascending order) moves
+ * to the k-th free page below n, in both pools and every layer; table and
+ * refs follow. move_src, move_dst [pages]: the moves made, then -1.
+ */
+pbs_status pbs_cache_compact(void *k_pages, void *v_pages, int32_t *table, int32_t *refs,
+                             int32_t *move_src, int32_t *move_dst, pbs_cache c, void *ws,
+                             size_t ws_bytes, pbs_stream_t st);
+
+/*
+ * pbs_cache_accept - the accepted drafts of each sequence moved behind its
+ * prefix: token start[s] + path[s][i] becomes token start[s] + i for i <
+ * count[s] (all `tree` when count is NULL), in both pools and every layer.
+ * path [seqs, tree] ascends strictly, 0 <= path < tree, so a draft only
+ * moves down; a sequence whose path does not, is reported and left alone.
+ * lens (may be NULL): lens[s] = start[s] + count[s] where the path is good.
+ */
+pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,
+                            const int32_t *start, const int32_t *path, const int32_t *count,
+                            int32_t *lens, int tree, pbs_cache c, pbs_stream_t st);
+
+/*
+ * pbs_tree_mask - which drafts see which, from their parents. parents
+ * [batch, tree]: the draft that draft i continues, parents[i] < i, or -1 for
+ * the cached prefix. Bit j & 31 of mask[b][i][j >> 5] (mask [batch, tree,
+ * ceil(tree / 32)] uint32) is set when j is i or an ancestor of i; depth
+ * [batch, tree] (may be NULL) counts the ancestors. A parent out of range is
+ * reported and read as -1. tree <= 1024.
+ */
+pbs_status pbs_tree_mask(const int32_t *parents, uint32_t *mask, int32_t *depth, int batch,
+                         int tree, pbs_stream_t st);
+
+/*
+ * pbs_tree_attn - attention of up to `tree` drafted tokens per sequence over
+ * the cache. Draft i < count[s] (all `tree` when count is NULL) sees tokens
+ * 0 .. start[s]-1 and those tokens start[s] + j, j < count[s], whose bit is
+ * set in mask row i (mask NULL: j <= i, a chain). With tree == 1 this is a
+ * decoding step. Logits sigma * q . k, softmax and output in fp32, the
+ * weights split into two 16-bit parts for the second product.
+ *
+ *   q    [seqs, hq, tree, d] (layer stride unused), bf16 or fp16
+ *   k_pages, v_pages [pages, hkv, page, d]: one layer (c.layers is ignored);
+ *        page a power of two from 16 to 256, d 64 or 128, pages * hkv * page
+ *        below 2^31, hq a multiple of hkv, tree <= 1024, seqs <= 2048
+ *   out  [seqs, hq, tree, d] dense; lse [seqs, hq, tree] fp32 or NULL, natural
+ *        logarithm. A row that sees nothing becomes 0 with lse = -inf; rows
+ *        i >= count[s] are left as they were.
+ * A token that a row does not see has no part in it, whatever its K and V
+ * hold (NaN and infinities too).
+ */
+pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
+                         const int32_t *table, const int32_t *start, const int32_t *count,
+                         const uint32_t *mask, void *out, float *lse, int hq, int tree,
+                         pbs_cache c, float scale, int dtype, void *ws, size_t ws_bytes,
+                         pbs_stream_t st);
+
+/* Bytes of device workspace pbs_tree_attn needs (0 for a refused shape); they
+ * depend on the device's SM count, hq, tree and c, not on the lengths. */
+size_t pbs_tree_workspace_bytes(int hq, int tree, pbs_cache c);
 
 /*
  * Synchronises `st`, returns in *code the current device's error word

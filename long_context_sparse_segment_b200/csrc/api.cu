@@ -10,6 +10,7 @@
 
 #include "../../include/pbs.h"
 #include "common.cuh"
+#include "decode.h"
 #include "internal.h"
 
 namespace pbs {
@@ -24,6 +25,8 @@ constexpr int kMaxDevices = 64;
 int *g_err_ptr[kMaxDevices];
 std::once_flag g_err_once[kMaxDevices];
 
+}  // namespace
+
 int *error_word() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
@@ -33,8 +36,6 @@ int *error_word() {
   });
   return g_err_ptr[dev];
 }
-
-}  // namespace
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -512,6 +513,7 @@ const char *pbs_status_string(int status) {
     case PBS_ERR_TIMEOUT: return "PBS_ERR_TIMEOUT";
     case PBS_ERR_DEVICE_ASSERT: return "PBS_ERR_DEVICE_ASSERT";
     case PBS_ERR_WORKSPACE: return "PBS_ERR_WORKSPACE";
+    case PBS_ERR_PAGES: return "PBS_ERR_PAGES";
     default: return "PBS_ERR_UNKNOWN";
   }
 }

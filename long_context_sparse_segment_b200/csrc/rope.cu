@@ -1,0 +1,185 @@
+// Rotary positions of Q and K in one launch (pbs_rope).
+//
+// A pair (x0, x1) of a row at position t turns by a = t f:
+//   y0 = g (x0 cos a - x1 sin a),  y1 = g (x1 cos a + x0 sin a).
+// The work is one read and one write of every element, so the kernel is
+// bound by memory (small batches: by latency). A token's angles are the
+// same in every head: a thread computes the cosines and sines of its pairs
+// once and walks the heads with them.
+//
+// Angles. t f in fp32 is off by up to t f 2^-24 radians (0.008 at 131072),
+// more than a bf16 result's rounding, and fp64 sine and cosine are slow. So
+// f is turned into a 64-bit fixed-point fraction of a turn; t times it in
+// integers, modulo 2^64, is the angle modulo one turn without rounding, and
+// its upper 32 bits go through sincospif. What is left is f's own rounding
+// (2^-53 relative, times t) and fp32's 2^-24 of half a turn.
+#include "common.cuh"
+#include "decode.h"
+
+#include <cuda_fp16.h>
+
+namespace pbs {
+namespace {
+
+constexpr int kThreads = 128;
+
+struct RopeArgs {
+  pbs_rows q, qo, k, ko;
+  const int32_t *pos;
+  const double *inv_freq;
+  int64_t pos_batch, tokens;
+  float gain;
+  int hq, heads, n, d, rot, heads_per, transpose;
+};
+
+template <typename T>
+struct Vec {  // 16 bytes of T as fp32
+  static constexpr int V = 16 / sizeof(T);
+};
+
+__device__ __forceinline__ void unpack(const uint4 &u, float (&x)[8], __nv_bfloat16) {
+  const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(p[i]);
+    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void unpack(const uint4 &u, float (&x)[8], __half) {
+  const __half2 *p = reinterpret_cast<const __half2 *>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(p[i]);
+    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void unpack(const uint4 &u, float (&x)[4], float) {
+  x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y);
+  x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[8], __nv_bfloat16) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                    pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[8], __half) {
+  uint4 u;
+  __half2 *p = reinterpret_cast<__half2 *>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+  return u;
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[4], float) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                    __float_as_uint(x[3]));
+}
+
+// A unit is two 16-byte vectors of a head's row. HALF: a rotated unit u
+// holds elements [uV, uV + V) and the same from rot/2 on; else the 2V
+// elements from 2uV on, V pairs side by side. Units behind rot are copied.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int V = Vec<T>::V;
+  const int units = a.d / (2 * V);
+  const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t token = at / units;
+  if (token >= a.tokens) return;
+  const int u = (int)(at - token * units);
+  const int64_t b = token / a.n, i = token - b * a.n;
+  const bool turns = 2 * u * V < a.rot;
+  const int lo = HALF && turns ? u * V : 2 * u * V;
+  const int hi = HALF && turns ? a.rot / 2 + u * V : lo + V;
+  float c[V], s[V];
+  if (turns) {
+    const uint64_t t = (uint64_t)(int64_t)__ldg(a.pos + b * a.pos_batch + i);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      double f = __ldg(a.inv_freq + u * V + e) * 0.15915494309189535;  // turns per position
+      f -= floor(f);
+      const uint64_t angle = t * (uint64_t)(f * 18446744073709551616.0);
+      // upper 32 bits as a signed fraction: half turns in [-1, 1)
+      sincospif((float)(int32_t)(angle >> 32) * 4.656612873077393e-10f, &s[e], &c[e]);
+      c[e] *= a.gain;
+      s[e] *= a.transpose ? -a.gain : a.gain;
+    }
+  }
+  const int h0 = blockIdx.y * a.heads_per, h1 = min(h0 + a.heads_per, a.heads);
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    const bool is_q = h < a.hq;
+    const pbs_rows &x = is_q ? a.q : a.k, &y = is_q ? a.qo : a.ko;
+    const int hh = is_q ? h : h - a.hq;
+    const T *src = (const T *)x.p + b * x.batch + hh * x.head + i * x.row;
+    T *dst = (T *)y.p + b * y.batch + hh * y.head + i * y.row;
+    uint4 v0 = *reinterpret_cast<const uint4 *>(src + lo);
+    uint4 v1 = *reinterpret_cast<const uint4 *>(src + hi);
+    if (turns) {
+      float x0[V], x1[V], y0[V], y1[V];
+      unpack(v0, x0, T());
+      unpack(v1, x1, T());
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (HALF) {
+          y0[e] = x0[e] * c[e] - x1[e] * s[e];
+          y1[e] = x1[e] * c[e] + x0[e] * s[e];
+        } else {  // pair e: elements 2e, 2e + 1 of the unit's 2V
+          const float p = 2 * e < V ? x0[2 * e % V] : x1[2 * e % V];
+          const float r = 2 * e < V ? x0[2 * e % V + 1] : x1[2 * e % V + 1];
+          (2 * e < V ? y0 : y1)[2 * e % V] = p * c[e] - r * s[e];
+          (2 * e < V ? y0 : y1)[2 * e % V + 1] = r * c[e] + p * s[e];
+        }
+      }
+      v0 = pack(y0, T());
+      v1 = pack(y1, T());
+    }
+    *reinterpret_cast<uint4 *>(dst + lo) = v0;
+    *reinterpret_cast<uint4 *>(dst + hi) = v1;
+  }
+}
+
+template <typename T>
+void launch(const RopeArgs &a, dim3 grid, bool half, cudaStream_t st) {
+  if (half)
+    rope_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
+  else
+    rope_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
+}
+
+}  // namespace
+}  // namespace pbs
+
+using namespace pbs;
+
+extern "C" pbs_status pbs_rope(pbs_rows q, pbs_rows q_out, int hq, pbs_rows k, pbs_rows k_out,
+                               int hkv, const int32_t *pos, int64_t pos_batch,
+                               const double *inv_freq, float gain, int batch, int n, int d,
+                               int rot, int layout, int transpose, int dtype, pbs_stream_t st) {
+  if (batch < 0 || n < 0 || hq < 0 || hkv < 0 || hq > (1 << 20) || hkv > (1 << 20) || d < 16 ||
+      d > 1024 || d % 16 || rot < 0 || rot > d || rot % 16 || layout < 0 || layout > 1 ||
+      dtype < PBS_BF16 || dtype > PBS_FP32)
+    return PBS_ERR_INVALID_ARG;
+  if (batch == 0 || n == 0 || hq + hkv == 0) return PBS_OK;
+  const int elem = dtype == PBS_FP32 ? 4 : 2;
+  if ((hq > 0 && (!rows_ok(q, elem) || !rows_ok(q_out, elem))) ||
+      (hkv > 0 && (!rows_ok(k, elem) || !rows_ok(k_out, elem))) || !pos ||
+      ((uintptr_t)pos & 3u) || (rot > 0 && (!inv_freq || ((uintptr_t)inv_freq & 7u))))
+    return PBS_ERR_INVALID_ARG;
+  RopeArgs a{q, q_out, k, k_out, pos, inv_freq, pos_batch, (int64_t)batch * n, gain};
+  a.hq = hq, a.heads = hq + hkv, a.n = n, a.d = d, a.rot = rot, a.transpose = transpose != 0;
+  const int64_t bx = ceil_div(a.tokens * (d * elem / 32), kThreads);
+  if (bx > 0x7fffffff) return PBS_ERR_UNSUPPORTED;
+  // few tokens: the heads are split over blocks until there are eight blocks
+  // an SM, and the angles computed again in each
+  int64_t split = ceil_div(148 * 8, bx);
+  if (split > a.heads) split = a.heads;
+  a.heads_per = (int)ceil_div(a.heads, split);
+  if (ceil_div(a.heads, a.heads_per) > 65535) return PBS_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)bx, (unsigned)ceil_div(a.heads, a.heads_per));
+  cudaStream_t cs = (cudaStream_t)st;
+  if (dtype == PBS_BF16)
+    launch<__nv_bfloat16>(a, grid, layout == 0, cs);
+  else if (dtype == PBS_FP16)
+    launch<__half>(a, grid, layout == 0, cs);
+  else
+    launch<float>(a, grid, layout == 0, cs);
+  return cudaGetLastError() == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}

@@ -1,0 +1,808 @@
+// Attention of a tree of drafted tokens over a paged K/V cache
+// (pbs_tree_mask, pbs_tree_attn).
+//
+// Draft i of sequence s sees the start[s] cached tokens and the drafts whose
+// bit its mask row has: o_i = sum_j softmax_j(sigma q_i . k_j) v_j. The G =
+// hq / hkv query heads of a KV head share its K and V, so the rows of one
+// work item are (draft i, head g), row r = i G + g: every cached row is read
+// once per item and serves them all. With few rows this is bound by reading
+// the cache.
+//
+// Work. The key tiles of all items (sequence, KV head, tile of rows) form
+// one line of units, cut into equal runs, one per CTA (one CTA per SM): a
+// ragged batch and a single long sequence load every SM alike, and the
+// lengths are read on the device. A run that holds all of an item's units
+// writes its rows; an item cut by a run's end leaves its running maximum,
+// sum and output (fp32) in the workspace, at most two per CTA, and the
+// combining kernel joins them in unit order, so results do not depend on
+// timing.
+//
+// This kernel: up to 32 rows an item, warp MMA. Eight warps take tiles of 64
+// keys, four warps a tile (16 keys each) and the two halves in turn, each
+// with its own maximum, sum and output, joined when the item ends; a ninth
+// warp brings the tiles by TMA, page by page, into a ring.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "decode.h"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace pbs {
+namespace {
+
+using namespace tc;
+
+constexpr int kMaxSeqs = 2048;   // the units before each sequence stay in shared memory
+constexpr int kMaxTree = 1024;   // 32 mask words a row
+
+struct TreeArgs {
+  pbs_rows q;
+  const int32_t *table, *start, *count;
+  const uint32_t *mask;
+  const void *v_pages;  // for the non-finite rows of drafts
+  void *out;
+  float *lse;
+  float *part_o;    // [2 grid][rows][d]
+  float2 *part_ml;  // [2 grid][rows]: running maximum (log2) and sum
+  int *part_bad;    // [2 grid]: drafted V rows with NaN or infinity met
+  int *err;
+  int hq, hkv, G, tree, words, seqs, width, page, pages;
+  float sl2;
+};
+
+// What a sequence asks for: its cached tokens and drafts (0 where the call
+// has to leave it alone).
+struct Seq {
+  int start, count;
+};
+
+__device__ __forceinline__ Seq seq_of(const TreeArgs &a, int s) {
+  Seq q{__ldg(a.start + s), a.count ? min(__ldg(a.count + s), a.tree) : a.tree};
+  if (q.count <= 0) return {0, 0};
+  if (q.start < 0 || (int64_t)q.start + q.count > (int64_t)a.width * a.page) {
+    report(a.err, PBS_ERR_DEVICE_ASSERT);
+    return {0, 0};
+  }
+  return q;
+}
+
+__device__ __forceinline__ int cdiv(int x, int y) { return (x + y - 1) / y; }
+
+// Units of a sequence: its items (KV head, row tile) times its key tiles.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ int units_of(const TreeArgs &a, const Seq &q) {
+  return q.count ? a.hkv * cdiv(q.count * a.G, ROWS) * cdiv(q.start + q.count, KEYS) : 0;
+}
+
+// Inclusive sums over a block of NT threads (a multiple of 32).
+template <int NT>
+__device__ __forceinline__ int block_scan(int x, int *sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  int add = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) add += w < warp ? sh[w] : 0;
+  __syncthreads();
+  return x + add;
+}
+
+// before[s]: units of the sequences in front of s; before[seqs]: all.
+template <int ROWS, int KEYS, int NT>
+__device__ __forceinline__ void plan_units(const TreeArgs &a, int *before, int *sh) {
+  int base = 0;
+  for (int s0 = 0; s0 < a.seqs; s0 += NT) {
+    const int s = s0 + threadIdx.x;
+    const int x = s < a.seqs ? units_of<ROWS, KEYS>(a, seq_of(a, s)) : 0;
+    const int inc = block_scan<NT>(x, sh);
+    if (s < a.seqs) before[s] = base + inc - x;
+    if (threadIdx.x == NT - 1) sh[NT / 32] = inc;
+    __syncthreads();
+    base += sh[NT / 32];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) before[a.seqs] = base;
+  __syncthreads();
+}
+
+// The units of CTA c: [run_start(c), run_start(c + 1)); none is empty with
+// runs = min(total, CTAs) of them. The run that unit u belongs to.
+__device__ __forceinline__ int run_start(int total, int c, int runs) {
+  return (int)((int64_t)total * c / runs);
+}
+__device__ __forceinline__ int run_owner(int total, int u, int runs) {
+  return (int)((((int64_t)u + 1) * runs - 1) / total);
+}
+
+// A piece of a CTA's run inside one item.
+struct Segment {
+  int s, h, rt;      // sequence, KV head, row tile
+  int start, count;  // tokens, drafts
+  int k0, k1;        // key tiles
+  int whole;         // all of the item's key tiles
+};
+
+template <int ROWS, int KEYS>
+__device__ __forceinline__ Segment segment_at(const TreeArgs &a, const int *before, int u, int end,
+                                              int *s_hint) {
+  int s = *s_hint;
+  while (before[s + 1] <= u) ++s;
+  *s_hint = s;
+  const Seq q = seq_of(a, s);
+  const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(q.count * a.G, ROWS);
+  const int x = u - before[s], item = x / kt;
+  Segment g;
+  g.s = s, g.h = item / rts, g.rt = item % rts;
+  g.start = q.start, g.count = q.count;
+  g.k0 = x - item * kt;
+  g.k1 = min(kt, g.k0 + end - u);
+  g.whole = g.k1 - g.k0 == kt;
+  return g;
+}
+
+// Whether draft i sees draft j (j < count).
+__device__ __forceinline__ bool sees(const TreeArgs &a, int s, int i, int j) {
+  if (!a.mask) return j <= i;
+  return __ldg(a.mask + ((size_t)s * a.tree + i) * a.words + (j >> 5)) >> (j & 31) & 1;
+}
+
+// ---------------------------------------------------------------- 16-bit types
+template <typename T>
+struct Two;
+template <>
+struct Two<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t pack(float x, float y) { return pack_bf16(x, y); }
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  static constexpr uint32_t kExp = 0x7f80u;
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+    mma_16816(c, a, b0, b1);
+  }
+};
+template <>
+struct Two<__half> {
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+  }
+  static constexpr uint32_t kExp = 0x7c00u;
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+        "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+
+// NaN or infinity in a 16-bit value.
+template <typename T>
+__device__ __forceinline__ bool wild16(uint32_t x) {
+  return (x & Two<T>::kExp) == Two<T>::kExp;
+}
+
+// The two halves of u that `keep` (bits 0, 1) has; with `drafted` (bits 0, 1)
+// a NaN or infinity in such a half becomes 0 and *bad is set.
+template <typename T>
+__device__ __forceinline__ uint32_t clean2(uint32_t u, unsigned keep, unsigned drafted, bool *bad) {
+  uint32_t lo = keep & 1 ? u & 0xffffu : 0, hi = keep & 2 ? u & 0xffff0000u : 0;
+  if ((drafted & 1) && wild16<T>(lo)) lo = 0, *bad = true;
+  if ((drafted & 2) && wild16<T>(hi >> 16)) hi = 0, *bad = true;
+  return lo | hi;
+}
+
+// The product P V leaves NaN and infinite values of drafted V rows out, since
+// 0 times them would reach the rows that do not see them. This adds them to a
+// row that does: columns [col, col + N) of draft i's output.
+template <typename T, int N>
+__device__ __noinline__ void add_wild(const TreeArgs &a, int s, int h, const Seq &q, int i,
+                                      int d, int col, float (&o)[N]) {
+  for (int j = 0; j < q.count; ++j) {
+    if (!sees(a, s, i, j)) continue;
+    const int t = q.start + j;
+    const int page = __ldg(a.table + (size_t)s * a.width + t / a.page);
+    if (page < 0 || page >= a.pages) continue;
+    const T *v = (const T *)a.v_pages +
+                 (((size_t)page * a.hkv + h) * a.page + t % a.page) * d + col;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float x = (float)v[e];
+      if (!isfinite(x)) o[e] += x;
+    }
+  }
+}
+
+// N output columns of row r of an item, from fp32.
+template <typename T, int N>
+__device__ __forceinline__ void write_row(const TreeArgs &a, int s, int h, int r, int d, int col,
+                                          const float (&o)[N]) {
+  const int i = r / a.G, g = r % a.G;
+  T *dst = (T *)a.out + (((size_t)s * a.hq + h * a.G + g) * a.tree + i) * d + col;
+  uint32_t p[N / 2];
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) p[e] = Two<T>::pack(o[2 * e], o[2 * e + 1]);
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(p[0], p[1], p[2], p[3]);
+  else if constexpr (N == 4)
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(p[0], p[1]);
+  else
+    *reinterpret_cast<uint32_t *>(dst) = p[0];
+}
+
+__device__ __forceinline__ void write_lse(const TreeArgs &a, int s, int h, int r, float m, float l) {
+  if (a.lse)
+    a.lse[((size_t)s * a.hq + h * a.G + r % a.G) * a.tree + r / a.G] =
+        l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// 2^(m - top) for a part whose maximum is m, top the maximum of all parts.
+__device__ __forceinline__ float part_scale(float m, float top) {
+  return m == top ? 1.f : ex2_approx(m - top);
+}
+
+// ------------------------------------------------------------- warp-MMA kernel
+constexpr int kKeys = 64;       // keys of a unit
+constexpr int kConsumers = 8;   // warps
+constexpr int kMmaThreads = 32 * (kConsumers + 1);
+
+template <int D, int MT>
+struct MmaCfg {
+  static constexpr int H = D / 64;
+  static constexpr int ROWS = 16 * MT;
+  static constexpr uint32_t KV = kKeys * D * 2;   // bytes of a K or V tile
+  static constexpr int ST = D == 128 ? 4 : 8;     // even: a stage stays with one half
+  static constexpr int PAD = 4;                   // floats behind a joined row
+  static constexpr size_t JOIN = (size_t)kConsumers * 16 * (D + PAD) * 4;
+  struct Bars {
+    uint64_t full[ST], empty[ST], join;
+    int abort, bad;
+    int sh[12];
+    float2 ml[kConsumers][ROWS];
+    int before[kMaxSeqs + 1];
+  };
+  static constexpr size_t SMEM = 1024 + 2 * KV * ST + ROWS * D * 2 + JOIN + sizeof(Bars);
+};
+static_assert(MmaCfg<128, 2>::SMEM <= 232448 && MmaCfg<64, 2>::SMEM <= 232448, "shared memory");
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    tree_mma_kernel(const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a) {
+  using C = MmaCfg<D, MT>;
+  constexpr int H = C::H, ST = C::ST, ROWS = C::ROWS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t *ring = base;                          // [ST][K tile, V tile]
+  T *sQ = reinterpret_cast<T *>(ring + 2 * C::KV * ST);
+  float *join = reinterpret_cast<float *>(sQ + ROWS * D);
+  auto *bar = reinterpret_cast<typename C::Bars *>(reinterpret_cast<uint8_t *>(join) + C::JOIN);
+  volatile int *abort = &bar->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) mbar_init(&bar->full[i], 1), mbar_init(&bar->empty[i], 4);
+    mbar_init(&bar->join, kConsumers);
+    bar->abort = 0, bar->bad = 0;
+    fence_barrier_init();
+  }
+  plan_units<ROWS, kKeys, kMmaThreads>(a, bar->before, bar->sh);
+  const int *before = bar->before;
+  const int total = before[a.seqs];
+  const int runs = min(total, (int)gridDim.x);
+  if ((int)blockIdx.x >= runs) return;
+  const int u0 = run_start(total, blockIdx.x, runs);
+  const int u1 = run_start(total, blockIdx.x + 1, runs);
+
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------- producer
+    // A unit is up to 4 boxes of page rows x 64 columns, H column halves, K
+    // and V: one lane each. Rows of a page behind the last token come along;
+    // pages behind it do not.
+    const int box = min(a.page, kKeys), pieces = kKeys / box;
+    const int kv = lane & 1, half = (lane >> 1) % H, piece = (lane >> 1) / H;
+    const bool mine = piece < pieces;
+    int hint = 0, it = 0;
+    bool ok = true;
+    if (lane == 0) prefetch_map(&tmK), prefetch_map(&tmV);
+    for (int u = u0; u < u1 && ok;) {
+      const Segment g = segment_at<ROWS, kKeys>(a, before, u, u1, &hint);
+      const int len = g.start + g.count;
+      const int32_t *row = a.table + (size_t)g.s * a.width;
+      for (int k = g.k0; k < g.k1; ++k, ++it) {
+        const int st = it % ST;
+        const int t = k * kKeys + piece * box;
+        const bool load = mine && t < len;
+        int y = 0;
+        if (load) {
+          int page = __ldg(row + t / a.page);
+          if (page < 0 || page >= a.pages) {
+            report(a.err, PBS_ERR_DEVICE_ASSERT);
+            page = 0;
+          }
+          y = (page * a.hkv + g.h) * a.page + t % a.page;
+        }
+        const int boxes = __popc(__ballot_sync(0xffffffffu, load));
+        if (it >= ST && !mbar_wait_warp(&bar->empty[st], (it / ST - 1) & 1, abort, a.err, 11)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_expect_tx(&bar->full[st], boxes * box * 128);
+        __syncwarp();
+        if (load)
+          tma_load_2d(ring + (size_t)(2 * st + kv) * C::KV + half * (kKeys * 128) +
+                          piece * box * 128,
+                      kv ? &tmV : &tmK, &bar->full[st], half * 64, y);
+        __syncwarp();
+      }
+      u += g.k1 - g.k0;
+    }
+    // every copy started here lands before the CTA exits
+    int never = 0;
+    for (int i = it > ST ? it - ST : 0; i < it; ++i)
+      mbar_wait(&bar->full[i % ST], (i / ST) & 1, &never, nullptr);
+    return;
+  }
+
+  // --------------------------------------------------------------- consumers
+  const int half_id = warp >> 2, key16 = (warp & 3) * 16;
+  const int gr = lane >> 2, qc = (lane & 3) * 2;
+  uint32_t phase = 0;
+  auto sync = [&]() {  // the eight warps
+    warp_arrive(&bar->join, lane);
+    const bool ok = mbar_wait_warp(&bar->join, phase, abort, a.err, 51);
+    phase ^= 1;
+    return ok;
+  };
+  int hint = 0, it = 0;
+  for (int u = u0; u < u1;) {
+    const Segment g = segment_at<ROWS, kKeys>(a, before, u, u1, &hint);
+    const int rows = min(ROWS, g.count * a.G - g.rt * ROWS);  // of this row tile
+    const int len = g.start + g.count;
+    // Q rows into shared memory, 16-byte chunks XOR-swizzled by row
+    for (int x = tid; x < ROWS * (D / 8); x += 32 * kConsumers) {
+      const int r = x / (D / 8), ch = x % (D / 8);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int rr = g.rt * ROWS + r, i = rr / a.G, hd = g.h * a.G + rr % a.G;
+        v = *reinterpret_cast<const uint4 *>((const T *)a.q.p + (int64_t)g.s * a.q.batch +
+                                             hd * a.q.head + i * a.q.row + ch * 8);
+      }
+      *reinterpret_cast<uint4 *>(sQ + swz<D>(r, ch * 8)) = v;
+    }
+    if (tid == 0) bar->bad = 0;
+    if (!sync()) return;
+    // drafts of this thread's rows
+    int draft[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        draft[mt][x] = min((g.rt * ROWS + mt * 16 + gr + 8 * x) / a.G, g.count - 1);
+    float m[MT][2], l[MT][2], o[MT][D / 8][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) m[mt][x] = -INFINITY, l[mt][x] = 0.f;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+    }
+    bool bad = false;
+    for (int k = g.k0; k < g.k1; ++k, ++it) {
+      if ((it & 1) != half_id) continue;
+      const int st = it % ST;
+      if (!mbar_wait_warp(&bar->full[st], (it / ST) & 1, abort, a.err, 41)) return;
+      const uint8_t *tK = ring + (size_t)(2 * st) * C::KV, *tV = tK + C::KV;
+      const int key0 = k * kKeys + key16;  // this warp's 16 keys
+      if (key0 < len) {
+        // S = Q K^T
+        float s[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+        {
+          const int row = key16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int ch = kk * 2 + ((lane >> 3) & 1);
+            uint32_t b[4];
+            ldsm_x4(b, tK + (ch >> 3) * (kKeys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t q[4];
+              ldsm_x4(q, sQ + swz<D>(mt * 16 + (lane & 15), kk * 16 + ((lane >> 4) << 3)));
+              Two<T>::mma(s[mt][0], q, b[0], b[1]);
+              Two<T>::mma(s[mt][1], q, b[2], b[3]);
+            }
+          }
+        }
+        // masks: drafts, and keys behind the last token
+        if (key0 + 16 > g.start) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int j = key0 + n * 8 + qc + (e & 1) - g.start;
+                if (j >= 0 && (j >= g.count || !sees(a, g.s, draft[mt][e >> 1], j)))
+                  s[mt][n][e] = -INFINITY;
+              }
+        }
+        // running maximum, P in two 16-bit parts: 16 bits alone would add as
+        // much error as the output's own rounding
+        uint32_t hi[MT][4], lo[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float alpha[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float t = fmaxf(fmaxf(s[mt][0][2 * x], s[mt][0][2 * x + 1]),
+                            fmaxf(s[mt][1][2 * x], s[mt][1][2 * x + 1]));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+            const float top = fmaxf(m[mt][x], t * a.sl2);
+            alpha[x] = m[mt][x] == top ? 1.f : ex2_approx(m[mt][x] - top);
+            m[mt][x] = top;
+            const float mu = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float p0 = ex2_approx(fmaf(s[mt][n][2 * x], a.sl2, -mu));
+              const float p1 = ex2_approx(fmaf(s[mt][n][2 * x + 1], a.sl2, -mu));
+              sum += p0 + p1;
+              const uint32_t h = Two<T>::pack(p0, p1);
+              const float2 f = Two<T>::unpack(h);
+              hi[mt][2 * n + x] = h;
+              lo[mt][2 * n + x] = Two<T>::pack(p0 - f.x, p1 - f.y);
+            }
+            l[mt][x] = l[mt][x] * alpha[x] + sum;
+          }
+          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[mt][n][e] *= alpha[e >> 1];
+          }
+        }
+        // O += P V; V rows behind the last token are left out, and NaN or
+        // infinity in a drafted row (see add_wild)
+        const bool edge = key0 + 16 > g.start;
+        unsigned keep[2] = {3, 3}, drafted[2] = {0, 0};
+        if (edge) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int t = key0 + qc + 8 * x;
+            keep[x] = (t < len) | (t + 1 < len) << 1;
+            drafted[x] = (t >= g.start) | (t + 1 >= g.start) << 1;
+          }
+        }
+        const int row = key16 + (lane & 15);
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          const int ch = n * 2 + (lane >> 4);
+          uint32_t b[4];
+          ldsm_x4_t(b, tV + (ch >> 3) * (kKeys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+          if (edge) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) b[x] = clean2<T>(b[x], keep[x & 1], drafted[x & 1], &bad);
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            Two<T>::mma(o[mt][2 * n], hi[mt], b[0], b[1]);
+            Two<T>::mma(o[mt][2 * n + 1], hi[mt], b[2], b[3]);
+            Two<T>::mma(o[mt][2 * n], lo[mt], b[0], b[1]);
+            Two<T>::mma(o[mt][2 * n + 1], lo[mt], b[2], b[3]);
+          }
+        }
+      }
+      warp_arrive(&bar->empty[st], lane);
+    }
+    // ------------------------------------------------ join the eight warps
+    if (__any_sync(0xffffffffu, bad) && lane == 0) bar->bad = 1;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float t = l[mt][x];
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        if ((lane & 3) == 0) bar->ml[warp][mt * 16 + gr + 8 * x] = make_float2(m[mt][x], t);
+      }
+    const int slot = 2 * blockIdx.x + (u != u0);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      if (mt * 16 < rows) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (mt * 16 + gr + 8 * x < rows)
+              *reinterpret_cast<float2 *>(join + (warp * 16 + gr + 8 * x) * (D + C::PAD) + n * 8 +
+                                          qc) = make_float2(o[mt][n][2 * x], o[mt][n][2 * x + 1]);
+      }
+      if (!sync()) return;
+      constexpr int N = D / 16;  // columns a thread joins: 16 threads a row
+      const int r = mt * 16 + (tid >> 4), col = (tid & 15) * N;
+      if (r < rows) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, bar->ml[w][r].x);
+        float sum = 0.f, acc[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+          const float2 ml = bar->ml[w][r];
+          const float f = part_scale(ml.x, top);
+          const float *src = join + (w * 16 + (r & 15)) * (D + C::PAD) + col;
+          sum += ml.y * f;
+#pragma unroll
+          for (int e = 0; e < N; e += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(src + e);
+            acc[e] += v.x * f, acc[e + 1] += v.y * f;
+            acc[e + 2] += v.z * f, acc[e + 3] += v.w * f;
+          }
+        }
+        const int rr = g.rt * ROWS + r;
+        if (g.whole) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] *= inv;
+          if (*(volatile int *)&bar->bad)
+            add_wild<T, N>(a, g.s, g.h, Seq{g.start, g.count}, rr / a.G, D, col, acc);
+          write_row<T, N>(a, g.s, g.h, rr, D, col, acc);
+          if (col == 0) write_lse(a, g.s, g.h, rr, top, sum);
+        } else {
+          float *dst = a.part_o + ((size_t)slot * ROWS + r) * D + col;
+#pragma unroll
+          for (int e = 0; e < N; e += 4)
+            *reinterpret_cast<float4 *>(dst + e) =
+                make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+          if (col == 0) a.part_ml[(size_t)slot * ROWS + r] = make_float2(top, sum);
+          if (tid == 0 && mt == 0) a.part_bad[slot] = bar->bad;
+        }
+      }
+      if (!sync()) return;  // the join buffer and Q are free again
+    }
+    u += g.k1 - g.k0;
+  }
+}
+
+// -------------------------------------------------------------------- combine
+// One warp per row of an item that several CTAs worked on: their parts, in
+// order, scaled to the common maximum. Bound by latency: a part is read once.
+constexpr int kCombineThreads = 128;
+
+template <typename T, int D, int ROWS, int KEYS>
+__global__ void __launch_bounds__(kCombineThreads)
+    tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
+  __shared__ int sh[8];
+  const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Seq q = seq_of(a, s);
+  if (blockIdx.x * 4 >= q.count * a.G) return;
+  // units before this sequence, and all
+  int mine = 0, all = 0;
+  for (int i = tid; i < a.seqs; i += kCombineThreads) {
+    const int x = units_of<ROWS, KEYS>(a, seq_of(a, i));
+    all += x;
+    if (i < s) mine += x;
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (lane == 0) sh[warp] = mine, sh[4 + warp] = all;
+  __syncthreads();
+  const int r = blockIdx.x * 4 + warp;  // row of the (sequence, KV head)
+  if (r >= q.count * a.G) return;
+  const int total = sh[4] + sh[5] + sh[6] + sh[7], runs = min(total, grid);
+  const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(q.count * a.G, ROWS);
+  const int u0 = sh[0] + sh[1] + sh[2] + sh[3] + (h * rts + r / ROWS) * kt;
+  const int c0 = run_owner(total, u0, runs), c1 = run_owner(total, u0 + kt - 1, runs);
+  if (c0 == c1) return;
+  const int slot0 = 2 * c0 + (run_start(total, c0, runs) != u0);
+  auto slot = [&](int c) { return c == c0 ? slot0 : 2 * c; };
+  const int rr = r % ROWS;
+  float top = -INFINITY;
+  int bad = 0;
+  for (int c = c0 + lane; c <= c1; c += 32) {
+    top = fmaxf(top, a.part_ml[(size_t)slot(c) * ROWS + rr].x);
+    bad |= a.part_bad[slot(c)];
+  }
+  top = warp_max(top);
+  bad = __any_sync(0xffffffffu, bad);
+  constexpr int N = D / 32;
+  const int col = lane * N;
+  float acc[N], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const size_t at = (size_t)slot(c) * ROWS + rr;
+    const float2 ml = a.part_ml[at];
+    const float f = part_scale(ml.x, top);
+    sum += ml.y * f;
+    const float *src = a.part_o + at * D + col;
+    if constexpr (N == 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(src);
+      acc[0] += v.x * f, acc[1] += v.y * f, acc[2] += v.z * f, acc[3] += v.w * f;
+    } else {
+      const float2 v = *reinterpret_cast<const float2 *>(src);
+      acc[0] += v.x * f, acc[1] += v.y * f;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] *= inv;
+  if (bad) add_wild<T, N>(a, s, h, q, r / a.G, D, col, acc);
+  write_row<T, N>(a, s, h, r, D, col, acc);
+  if (lane == 0) write_lse(a, s, h, r, top, sum);
+}
+
+// ----------------------------------------------------------------- tree masks
+// A warp per draft walks its ancestors; lane w holds mask word w.
+__global__ void __launch_bounds__(256)
+    tree_mask_kernel(const int32_t *__restrict__ parents, uint32_t *mask, int32_t *depth, int tree,
+                     int words, int *err) {
+  __shared__ int par[kMaxTree];
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  for (int x = threadIdx.x; x < tree; x += 256) {
+    int p = parents[(size_t)b * tree + x];
+    if (p < -1 || p >= x) {
+      if (blockIdx.x == 0) report(err, PBS_ERR_DEVICE_ASSERT);
+      p = -1;
+    }
+    par[x] = p;
+  }
+  __syncthreads();
+  if (i >= tree) return;
+  uint32_t word = 0;
+  int n = -1;
+  for (int p = i; p >= 0; p = par[p], ++n)
+    if (p >> 5 == lane) word |= 1u << (p & 31);
+  if (lane < words) mask[((size_t)b * tree + i) * words + lane] = word;
+  if (depth && lane == 0) depth[(size_t)b * tree + i] = n;
+}
+
+// ------------------------------------------------------------------ host side
+bool tree_shape_ok(int hq, int tree, const pbs_cache &c) {
+  return hq >= 1 && c.hkv >= 1 && hq % c.hkv == 0 && tree >= 0 && c.seqs >= 0 && c.pages >= 1 &&
+         c.page >= 1 && c.width >= 1;
+}
+
+// What the kernels take, beyond what makes sense.
+bool tree_supported(int hq, int tree, const pbs_cache &c) {
+  if ((c.d != 64 && c.d != 128) || c.page < 16 || c.page > 256 || (c.page & (c.page - 1)) ||
+      tree > kMaxTree || c.seqs > kMaxSeqs || hq > 65536 || c.hkv > 65535 ||
+      (int64_t)c.pages * c.hkv * c.page >= (1ll << 31) ||
+      (int64_t)c.width * c.page >= (1ll << 31) - 2 * kMaxTree)
+    return false;
+  const int64_t rows = (int64_t)(hq / c.hkv) * tree;
+  // units of a call, at most (the smallest tiles)
+  return rows < (1 << 22) && (double)c.seqs * c.hkv * ceil_div(rows, 16) *
+                                     ceil_div((int64_t)c.width * c.page, kKeys) < 2e9;
+}
+
+int row_tile(int hq, int tree, const pbs_cache &c) {
+  return (int64_t)(hq / c.hkv) * tree <= 16 ? 16 : 32;
+}
+
+struct Parts {
+  size_t o, ml, bad, bytes;
+};
+Parts parts(int rows, int d) {
+  const size_t slots = 2 * (size_t)sm_count();
+  Parts p;
+  p.o = 0;
+  p.ml = slots * rows * d * 4;
+  p.bad = p.ml + slots * rows * 8;
+  p.bytes = p.bad + slots * 4;
+  return p;
+}
+
+template <typename T, int D, int MT>
+cudaError_t run_mma(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a,
+                    cudaStream_t st) {
+  using C = MmaCfg<D, MT>;
+  auto kern = tree_mma_kernel<T, D, MT>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int grid = sm_count();
+  kern<<<grid, kMmaThreads, C::SMEM, st>>>(mk, mv, a);
+  const dim3 cg((unsigned)ceil_div((int64_t)a.G * a.tree, 4), a.hkv, a.seqs);
+  tree_combine_kernel<T, D, C::ROWS, kKeys><<<cg, kCombineThreads, 0, st>>>(a, grid);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t run_tree(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int d,
+                     int rows, cudaStream_t st) {
+  if (d == 64)
+    return rows == 16 ? run_mma<T, 64, 1>(mk, mv, a, st) : run_mma<T, 64, 2>(mk, mv, a, st);
+  return rows == 16 ? run_mma<T, 128, 1>(mk, mv, a, st) : run_mma<T, 128, 2>(mk, mv, a, st);
+}
+
+}  // namespace
+}  // namespace pbs
+
+using namespace pbs;
+
+extern "C" {
+
+pbs_status pbs_tree_mask(const int32_t *parents, uint32_t *mask, int32_t *depth, int batch,
+                         int tree, pbs_stream_t st) {
+  if (batch < 0 || tree < 0) return PBS_ERR_INVALID_ARG;
+  if (tree > kMaxTree || batch > 65535) return PBS_ERR_UNSUPPORTED;
+  if (batch == 0 || tree == 0) return PBS_OK;
+  if (!parents || !mask || ((uintptr_t)parents & 3u) || ((uintptr_t)mask & 3u) ||
+      ((uintptr_t)depth & 3u))
+    return PBS_ERR_INVALID_ARG;
+  tree_mask_kernel<<<dim3((tree + 7) / 8, batch), 256, 0, (cudaStream_t)st>>>(
+      parents, mask, depth, tree, (tree + 31) / 32, error_word());
+  return cudaGetLastError() == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}
+
+size_t pbs_tree_workspace_bytes(int hq, int tree, pbs_cache c) {
+  if (!tree_shape_ok(hq, tree, c) || !tree_supported(hq, tree, c) || c.seqs == 0 || tree == 0)
+    return 0;
+  return parts(row_tile(hq, tree, c), c.d).bytes;
+}
+
+pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
+                         const int32_t *table, const int32_t *start, const int32_t *count,
+                         const uint32_t *mask, void *out, float *lse, int hq, int tree,
+                         pbs_cache c, float scale, int dtype, void *ws, size_t ws_bytes,
+                         pbs_stream_t st) {
+  if (!tree_shape_ok(hq, tree, c) || (dtype != PBS_BF16 && dtype != PBS_FP16))
+    return PBS_ERR_INVALID_ARG;
+  if (!tree_supported(hq, tree, c)) return PBS_ERR_UNSUPPORTED;
+  if (c.seqs == 0 || tree == 0) return PBS_OK;
+  auto ints = [](const void *p) { return p && ((uintptr_t)p & 3u) == 0; };
+  if (!rows_ok(q, 2) || !aligned16(k_pages) || !aligned16(v_pages) || !k_pages || !v_pages ||
+      !ints(table) || !ints(start) || (count && !ints(count)) || (mask && !ints(mask)) || !out ||
+      !aligned16(out) || ((uintptr_t)lse & 3u) || !ws || !aligned16(ws))
+    return PBS_ERR_INVALID_ARG;
+  const int rows = row_tile(hq, tree, c);
+  const Parts p = parts(rows, c.d);
+  if (ws_bytes < p.bytes) return PBS_ERR_WORKSPACE;
+  TreeArgs a{};
+  a.q = q, a.table = table, a.start = start, a.count = count, a.mask = mask, a.v_pages = v_pages;
+  a.out = out, a.lse = lse;
+  a.part_o = (float *)((uint8_t *)ws + p.o);
+  a.part_ml = (float2 *)((uint8_t *)ws + p.ml);
+  a.part_bad = (int *)((uint8_t *)ws + p.bad);
+  a.err = error_word();
+  a.hq = hq, a.hkv = c.hkv, a.G = hq / c.hkv, a.tree = tree, a.words = (tree + 31) / 32;
+  a.seqs = c.seqs, a.width = c.width, a.page = c.page, a.pages = c.pages;
+  const float sigma = scale > 0.f ? scale : (float)(1.0 / sqrt((double)c.d));
+  a.sl2 = sigma * kLog2e;
+  CUtensorMap mk, mv;
+  const uint64_t all = (uint64_t)c.pages * c.hkv * c.page;
+  const int box = c.page < kKeys ? c.page : kKeys;
+  if (!make_tile_map(&mk, k_pages, all, c.d, box) || !make_tile_map(&mv, v_pages, all, c.d, box))
+    return PBS_ERR_CUDA;
+  cudaStream_t cs = (cudaStream_t)st;
+  const cudaError_t e = dtype == PBS_BF16 ? run_tree<__nv_bfloat16>(mk, mv, a, c.d, rows, cs)
+                                          : run_tree<__half>(mk, mv, a, c.d, rows, cs);
+  return e == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}
+
+}  // extern "C"

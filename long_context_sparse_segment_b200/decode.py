@@ -1,0 +1,440 @@
+"""PyTorch-facing calls of libpbs around the prefill: rotary positions, the
+paged K/V cache, and attention for trees of drafted tokens over it.
+
+As in ``ops.py`` every step runs in the library's CUDA kernels (csrc/rope.cu,
+cache.cu, tree.cu); these functions check tensors, allocate outputs and pass
+pointers and the current stream of the tensors' device through the C ABI
+(include/pbs.h). Nothing here waits for the device: lengths, page tables and
+reference counts are device tensors, so every call can be captured into a
+CUDA graph. What a kernel refuses (a bad page, a pool without free pages) is
+read with ``device_status``.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import _lib
+from ._lib import Cache, Rows, lib
+from .ops import _call, _ptr, _stream
+
+_TYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16, torch.float32: _lib.FP32}
+_LAYOUTS = {"half": 0, "pairs": 1}
+_HALVES = (torch.bfloat16, torch.float16)
+_NONE = Rows(None, 0, 0, 0, 0)
+
+
+def _on(t, name, device=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _ints(t, name, shape, device):
+    _on(t, name, device)
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name, written=False):
+    """[..., b, h, n, d] (4 or 5 dimensions) as pbs_rows: the head dimension
+    contiguous, the others multiples of 16 bytes."""
+    size, stride = t.shape, t.stride()
+    if size[-1] > 1 and stride[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    step = [st if n > 1 else 0 for n, st in zip(size[:-1], stride[:-1])]
+    vec = 16 // t.element_size()
+    if t.data_ptr() % 16 or any(x % vec for x in step):
+        raise ValueError(f"{name}: rows must be 16-byte aligned")
+    if written:
+        used = size[-1]
+        for st, n in sorted((st, n) for st, n in zip(stride[:-1], size[:-1]) if n > 1):
+            if st < used:
+                raise ValueError(f"{name}: an output may not overlap itself")
+            used = st * (n - 1) + used
+    return Rows(t.data_ptr(), step[0] if len(step) == 4 else 0, *step[-3:])
+
+
+def rope_freqs(rot, base=10000.0, scaling=None, device=None):
+    """(inv_freq [rot/2] fp64, gain) for ``rope``: inv_freq[i] = base^(-2i/rot)
+    radians per position, scaled for contexts longer than a model was trained
+    on (``original`` tokens) by ``factor``:
+
+    None                            as trained
+    dict(type="linear", factor=)    every frequency divided by factor
+    dict(type="ntk", factor=)       base * factor^(rot/(rot-2))
+    dict(type="ramp", factor=, original=, low=1, high=4)
+                                    pairs that turn more than ``high`` times in
+                                    ``original`` tokens keep their frequency,
+                                    those that turn less than ``low`` times
+                                    have it divided, a linear ramp over the
+                                    turns between
+    dict(type="yarn", factor=, original=, fast=32, slow=1, gain=None)
+                                    the same with the ramp over the pair's
+                                    index, and gain 0.1 ln(factor) + 1
+    """
+    if rot < 0 or rot % 16:
+        raise ValueError("rot must be a non-negative multiple of 16")
+    if not base > 0:
+        raise ValueError("base must be positive")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    freq = lambda b: torch.pow(torch.tensor(float(b), dtype=torch.float64), -2.0 * i / max(rot, 1))
+    f, gain = freq(base), 1.0
+    if scaling is not None:
+        s = dict(scaling)
+        kind, factor = s.pop("type"), float(s.pop("factor"))
+        if not factor >= 1:
+            raise ValueError("factor must be at least 1")
+        if kind == "linear":
+            f = f / factor
+        elif kind == "ntk":
+            f = freq(base * factor ** (rot / max(rot - 2, 1)))
+        elif kind == "ramp":
+            original, low, high = s.pop("original"), s.pop("low", 1.0), s.pop("high", 4.0)
+            if not high > low:
+                raise ValueError("high must be above low")
+            keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+            f = f * keep + f / factor * (1 - keep)
+        elif kind == "yarn":
+            original, fast, slow = s.pop("original"), s.pop("fast", 32.0), s.pop("slow", 1.0)
+            at = lambda turns: (rot * math.log(original / (turns * 2 * math.pi))
+                                / (2 * math.log(base)))
+            lo, hi = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rot - 1)
+            drop = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+            f = f / factor * drop + f * (1 - drop)
+            gain = s.pop("gain", None)
+            gain = 0.1 * math.log(factor) + 1.0 if gain is None else float(gain)
+        else:
+            raise ValueError(f"unknown scaling type {kind!r}")
+        if s:
+            raise ValueError(f"unknown scaling entries {sorted(s)}")
+    return f.to(device), gain
+
+
+def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=None, k_out=None):
+    """Rotary positions of q [b, hq, n, d] and k [b, hkv, n, d] (or None) in
+    one launch (pbs_rope): bf16, fp16 or fp32, any strides with contiguous
+    16-byte-aligned rows (slices of one projection). pos is int32 [b, n] or
+    [n]; the first 2 * len(inv_freq) elements of each head turn. ``transpose``
+    turns back: the gradients of q and k from those of the results. Returns
+    (q', k'), or q' alone without k. q_out, k_out may be q and k themselves."""
+    _on(q, "q")
+    dev = q.device
+    if q.dim() != 4:
+        raise ValueError("q must be [b, hq, n, d]")
+    if q.dtype not in _TYPES:
+        raise TypeError(f"q must be bf16, fp16 or fp32, got {q.dtype}")
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be 'half' or 'pairs', got {layout!r}")
+    b, hq, n, d = q.shape
+    if d < 16 or d % 16 or d > 1024:
+        raise ValueError("the head dimension must be a multiple of 16, at most 1024")
+    if k is not None:
+        _on(k, "k", dev)
+        if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (b, n, d) or k.dtype != q.dtype:
+            raise ValueError("k must be [b, hkv, n, d] of q's type")
+    _on(inv_freq, "inv_freq", dev)
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous fp64 vector")
+    rot = 2 * inv_freq.numel()
+    if rot % 16 or rot > d:
+        raise ValueError("inv_freq: 2 * len must be a multiple of 16 and at most d")
+    _ints(pos, "pos", (n,) if isinstance(pos, torch.Tensor) and pos.dim() == 1 else (b, n), dev)
+    outs = []
+    for x, y, nm in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if x is None:
+            if y is not None:
+                raise ValueError("k_out without k")
+            continue
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _on(y, nm, dev)
+            if y.shape != x.shape or y.dtype != x.dtype:
+                raise ValueError(f"{nm} must have the shape and type of its input")
+        outs.append(y)
+    if b and n and q.numel() + (k.numel() if k is not None else 0):
+        qr, qo = (_rows(q, "q"), _rows(outs[0], "q_out", True)) if hq else (_NONE, _NONE)
+        hkv = 0 if k is None else k.shape[1]
+        kr, ko = (_rows(k, "k"), _rows(outs[1], "k_out", True)) if hkv else (_NONE, _NONE)
+        with torch.cuda.device(dev):
+            _call("pbs_rope", qr, qo, hq, kr, ko, hkv, _ptr(pos), 0 if pos.dim() == 1 else n,
+                  _ptr(inv_freq), gain, b, n, d, rot, _LAYOUTS[layout], int(bool(transpose)),
+                  _TYPES[q.dtype], _stream(dev))
+    return outs[0] if k is None else tuple(outs)
+
+
+# ------------------------------------------------------------------ the cache
+def _pools(k_pages, v_pages, table=None):
+    """The pools [layers, pages, hkv, page, d] (or one layer's, 4-D)."""
+    _on(k_pages, "k_pages")
+    _on(v_pages, "v_pages", k_pages.device)
+    if k_pages.dim() not in (4, 5) or k_pages.element_size() != 2:
+        raise ValueError("k_pages must be [layers, pages, hkv, page, d] (or 4-D) of a 16-bit type")
+    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("v_pages must have the shape and type of k_pages")
+    if not k_pages.is_contiguous() or not v_pages.is_contiguous():
+        raise ValueError("k_pages and v_pages must be contiguous")
+    if k_pages.numel() == 0:
+        raise ValueError("k_pages is empty")
+    if k_pages.shape[-1] % 8:
+        raise ValueError("the head dimension must be a multiple of 8")
+    shape = k_pages.shape if k_pages.dim() == 5 else (1, *k_pages.shape)
+    seqs, width = (0, 1) if table is None else _table(table, k_pages.device)
+    return Cache(*shape, seqs, width)
+
+
+def _table(table, device=None):
+    _on(table, "table", device)
+    if table.dim() != 2 or table.shape[1] < 1:
+        raise ValueError("table must be [seqs, width]")
+    _ints(table, "table", table.shape, device)
+    return table.shape
+
+
+def _books(table, refs, lens, page):
+    seqs, width = _table(table)
+    _ints(refs, "refs", (refs.numel(),), table.device)
+    _ints(lens, "lens", (seqs,), table.device)
+    if refs.numel() < 1 or page < 1:
+        raise ValueError("refs and page must not be empty")
+    return Cache(1, refs.numel(), 1, page, 8, seqs, width)
+
+
+def _ws(op, c, n, device):
+    need = lib().pbs_cache_workspace_bytes(c, op, n)
+    return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
+
+
+def cache_reserve(table, refs, lens, want, page):
+    """Pages for the tokens lens[s] .. want[s]-1 of every sequence, each held
+    by it alone (pbs_cache_reserve). Returns (src, dst) int32 [seqs]: the
+    pages to copy with ``cache_copy`` before writing, -1 where none. Too few
+    free pages: nothing changes and device_status() is PBS_ERR_PAGES."""
+    c = _books(table, refs, lens, page)
+    dev = table.device
+    _ints(want, "want", (c.seqs,), dev)
+    src, dst = (torch.empty(c.seqs, dtype=torch.int32, device=dev) for _ in range(2))
+    ws, need = _ws(_lib.CACHE_RESERVE, c, 0, dev)
+    with torch.cuda.device(dev):
+        _call("pbs_cache_reserve", _ptr(table), _ptr(refs), _ptr(lens), _ptr(want), _ptr(src),
+              _ptr(dst), c, _ptr(ws), need, _stream(dev))
+    return src, dst
+
+
+def cache_append(k, v, k_pages, v_pages, table, start, count=None):
+    """Rows i < count[s] (all without count) of k, v [seqs, hkv, n, d] written
+    at tokens start[s] + i of one layer's pools, or [layers, seqs, hkv, n, d]
+    of all layers (pbs_cache_append). The pages must be reserved."""
+    c = _pools(k_pages, v_pages, table)
+    dev = k_pages.device
+    for t, nm in ((k, "k"), (v, "v")):
+        _on(t, nm, dev)
+        if t.dtype != k_pages.dtype or t.dim() != k_pages.dim():
+            raise ValueError(f"{nm} must have the type and dimensions of k_pages")
+        lead = (c.layers,) if t.dim() == 5 else ()
+        if t.shape != (*lead, c.seqs, c.hkv, k.shape[-2], c.d):
+            raise ValueError(f"{nm} must be {[*lead, c.seqs, c.hkv, 'n', c.d]}, got {list(t.shape)}")
+    _ints(start, "start", (c.seqs,), dev)
+    if count is not None:
+        _ints(count, "count", (c.seqs,), dev)
+    if k.numel() == 0:
+        return
+    with torch.cuda.device(dev):
+        _call("pbs_cache_append", _rows(k, "k"), _rows(v, "v"), k.shape[-2], _ptr(k_pages),
+              _ptr(v_pages), _ptr(table), _ptr(start), _ptr(count), c, _stream(dev))
+
+
+def cache_copy(k_pages, v_pages, src, dst):
+    """Page src[i] copied to page dst[i] in both pools and every layer; pairs
+    of -1 are skipped (pbs_cache_copy). All pairs happen at once: a repeated
+    destination, or a source that is also a destination, is refused on the
+    device."""
+    c = _pools(k_pages, v_pages)
+    dev = k_pages.device
+    _ints(src, "src", (src.numel(),), dev)
+    _ints(dst, "dst", (src.numel(),), dev)
+    n = src.numel()
+    ws, need = _ws(_lib.CACHE_COPY, c, n, dev)
+    with torch.cuda.device(dev):
+        _call("pbs_cache_copy", _ptr(k_pages), _ptr(v_pages), _ptr(src), _ptr(dst), n, c, _ptr(ws),
+              need, _stream(dev))
+
+
+def cache_fork(table, refs, lens, src, dst, page):
+    """Sequence dst[i] (empty) becomes a second holder of sequence src[i]'s
+    pages (pbs_cache_fork); no page is copied before one of them writes."""
+    c = _books(table, refs, lens, page)
+    dev = table.device
+    _ints(src, "src", (src.numel(),), dev)
+    _ints(dst, "dst", (src.numel(),), dev)
+    with torch.cuda.device(dev):
+        _call("pbs_cache_fork", _ptr(table), _ptr(refs), _ptr(lens), _ptr(src), _ptr(dst),
+              src.numel(), c, _stream(dev))
+
+
+def cache_trim(table, refs, lens, keep, page):
+    """Sequence s keeps min(lens[s], keep[s]) tokens and releases the pages
+    behind them; keep 0 frees it, a negative keep leaves it (pbs_cache_trim)."""
+    c = _books(table, refs, lens, page)
+    dev = table.device
+    _ints(keep, "keep", (c.seqs,), dev)
+    with torch.cuda.device(dev):
+        _call("pbs_cache_trim", _ptr(table), _ptr(refs), _ptr(lens), _ptr(keep), c, _stream(dev))
+
+
+def cache_compact(k_pages, v_pages, table, refs):
+    """The held pages moved to the low end of the pools; table and refs follow
+    (pbs_cache_compact). Returns (src, dst) int32 [pages]: the moves, then -1."""
+    c = _pools(k_pages, v_pages, table)
+    dev = k_pages.device
+    _ints(refs, "refs", (c.pages,), dev)
+    src, dst = torch.empty_like(refs), torch.empty_like(refs)
+    ws, need = _ws(_lib.CACHE_COMPACT, c, 0, dev)
+    with torch.cuda.device(dev):
+        _call("pbs_cache_compact", _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(refs), _ptr(src),
+              _ptr(dst), c, _ptr(ws), need, _stream(dev))
+    return src, dst
+
+
+def cache_accept(k_pages, v_pages, table, start, path, count=None, lens=None):
+    """The accepted drafts moved behind their prefix: token start[s] +
+    path[s][i] becomes token start[s] + i, i < count[s], in every layer
+    (pbs_cache_accept). path [seqs, tree] ascends strictly. With ``lens``,
+    lens[s] becomes start[s] + count[s]."""
+    c = _pools(k_pages, v_pages, table)
+    dev = k_pages.device
+    _ints(start, "start", (c.seqs,), dev)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise ValueError("path must be [seqs, tree]")
+    _ints(path, "path", (c.seqs, path.shape[1]), dev)
+    for t, nm in ((count, "count"), (lens, "lens")):
+        if t is not None:
+            _ints(t, nm, (c.seqs,), dev)
+    with torch.cuda.device(dev):
+        _call("pbs_cache_accept", _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(start),
+              _ptr(path), _ptr(count), _ptr(lens), path.shape[1], c, _stream(dev))
+
+
+# ------------------------------------------------------------------ attention
+def tree_mask(parents):
+    """(mask, depth) of drafted trees (pbs_tree_mask). parents int32 [b, tree]:
+    the draft that draft i continues (below i), or -1 for the cached prefix.
+    mask int32 [b, tree, ceil(tree/32)]: bit j & 31 of word j >> 5 of row i is
+    set when j is i or an ancestor of i; depth int32 [b, tree] counts the
+    ancestors (draft i's position is start + depth)."""
+    _on(parents, "parents")
+    if parents.dim() != 2:
+        raise ValueError("parents must be [b, tree]")
+    _ints(parents, "parents", parents.shape, parents.device)
+    b, t = parents.shape
+    mask = torch.empty(b, t, (t + 31) // 32, dtype=torch.int32, device=parents.device)
+    depth = torch.empty_like(parents)
+    with torch.cuda.device(parents.device):
+        _call("pbs_tree_mask", _ptr(parents), _ptr(mask), _ptr(depth), b, t,
+              _stream(parents.device))
+    return mask, depth
+
+
+def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.0, lse=False,
+              out=None, ws=None):
+    """Attention of q [seqs, hq, tree, d] (bf16 or fp16, strided rows) over one
+    layer's pools [pages, hkv, page, d] (pbs_tree_attn). Draft i < count[s]
+    (all without count) sees the first start[s] tokens and those tokens
+    start[s] + j, j < count[s], whose bit is set in mask row i (see
+    ``tree_mask``; without mask j <= i). With tree = 1 this is a decoding
+    step. Returns o [seqs, hq, tree, d], and lse [seqs, hq, tree] fp32 when
+    asked; rows i >= count[s] are left as they were in ``out`` and are zero
+    in what this call allocates (their lse too)."""
+    c = _pools(k_pages, v_pages, table)
+    dev = k_pages.device
+    _on(q, "q", dev)
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be one layer's: [pages, hkv, page, d]")
+    if q.dtype not in _HALVES or q.dtype != k_pages.dtype:
+        raise TypeError("q must be bf16 or fp16 and have the type of k_pages")
+    if q.dim() != 4 or q.shape[0] != c.seqs or q.shape[3] != c.d:
+        raise ValueError(f"q must be [{c.seqs}, hq, tree, {c.d}]")
+    _, hq, tree, d = q.shape
+    if hq < 1 or hq % c.hkv:
+        raise ValueError("hq must be a multiple of hkv")
+    _ints(start, "start", (c.seqs,), dev)
+    if count is not None:
+        _ints(count, "count", (c.seqs,), dev)
+    if mask is not None:
+        _ints(mask, "mask", (c.seqs, tree, (tree + 31) // 32), dev)
+    make = torch.empty if count is None else torch.zeros
+    if out is None:
+        out = make(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _on(out, "out", dev)
+        if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of q's shape and type")
+        if out.data_ptr() == q.data_ptr() and out.numel():
+            raise ValueError("out must not be q")
+    l = make(q.shape[:3], dtype=torch.float32, device=dev) if lse else None
+    need = lib().pbs_tree_workspace_bytes(hq, tree, c) if q.numel() else 0
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    rows = _rows(q, "q") if q.numel() else _NONE
+    with torch.cuda.device(dev):
+        _call("pbs_tree_attn", rows, _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(start),
+              _ptr(count), _ptr(mask), _ptr(out), _ptr(l), hq, tree, c, scale, _TYPES[q.dtype],
+              _ptr(ws), need, _stream(dev))
+    return (out, l) if lse else out
+
+
+class PagedCache:
+    """The tensors of a paged cache, and the calls above on them: pools k, v
+    [layers, pages, hkv, page, d], table [seqs, width], refs [pages], lens
+    [seqs]. Made empty; everything it knows is in these tensors."""
+
+    def __init__(self, seqs, max_len, pages, hkv, d, page=64, layers=1, dtype=torch.bfloat16,
+                 device="cuda"):
+        if min(seqs, max_len, pages, hkv, d, page, layers) < 1:
+            raise ValueError("sizes must be positive")
+        self.page = page
+        self.k = torch.zeros(layers, pages, hkv, page, d, dtype=dtype, device=device)
+        self.v = torch.zeros_like(self.k)
+        ints = lambda *n: torch.zeros(*n, dtype=torch.int32, device=self.k.device)
+        self.table = ints(seqs, -(-max_len // page)) - 1
+        self.refs, self.lens = ints(pages), ints(seqs)
+
+    def reserve(self, want):
+        """Room for want[s] tokens in every sequence, shared pages that will
+        be written copied."""
+        src, dst = cache_reserve(self.table, self.refs, self.lens, want, self.page)
+        cache_copy(self.k, self.v, src, dst)
+
+    def append(self, layer, k, v, start=None, count=None):
+        """k, v [seqs, hkv, n, d] at tokens start[s].. (the length) of a layer.
+        The length is not changed: every layer appends at the same tokens."""
+        cache_append(k, v, self.k[layer], self.v[layer], self.table,
+                     self.lens if start is None else start, count)
+
+    def attend(self, layer, q, mask=None, start=None, **kw):
+        """tree_attn of a layer; ``start`` is the lengths when not given."""
+        return tree_attn(q, self.k[layer], self.v[layer], self.table,
+                         self.lens if start is None else start, mask, **kw)
+
+    def accept(self, path, count=None):
+        """The accepted drafts behind the lengths, which grow by their number."""
+        start = self.lens.clone()
+        cache_accept(self.k, self.v, self.table, start, path, count, self.lens)
+
+    def fork(self, src, dst):
+        cache_fork(self.table, self.refs, self.lens, src, dst, self.page)
+
+    def trim(self, keep):
+        cache_trim(self.table, self.refs, self.lens, keep, self.page)
+
+    def compact(self):
+        return cache_compact(self.k, self.v, self.table, self.refs)
