@@ -583,24 +583,26 @@ pbs_status pbs_tree_mask(const int32_t *parents, uint32_t *mask, int32_t *depth,
  * the cache. Draft i < count[s] (all `tree` when count is NULL) sees tokens
  * 0 .. start[s]-1 and those tokens start[s] + j, j < count[s], whose bit is
  * set in mask row i (mask NULL: j <= i, a chain). With tree == 1 this is a
- * decoding step. Logits sigma * q . k, softmax and output in fp32, the
- * weights split into two 16-bit parts for the second product.
+ * decoding step. Logits sigma * q . k, the softmax's maximum and sum and the
+ * output's sums are fp32; the weights are rounded to 16 bits for the second
+ * product (with hq / hkv * tree <= 16 they keep two 16-bit parts).
  *
  *   q    [seqs, hq, tree, d] (layer stride unused), bf16 or fp16
  *   k_pages, v_pages [pages, hkv, page, d]: one layer (c.layers is ignored);
  *        page a power of two from 16 to 256, d 64 or 128, pages * hkv * page
- *        below 2^31, hq a multiple of hkv, tree <= 1024, seqs <= 2048
+ *        below 2^31, hq a multiple of hkv, tree <= 1024, seqs < 65536
  *   out  [seqs, hq, tree, d] dense; lse [seqs, hq, tree] fp32 or NULL, natural
  *        logarithm. A row that sees nothing becomes 0 with lse = -inf; rows
- *        i >= count[s] are left as they were.
+ *        i >= count[s] are left as they were, or with zero_rest become 0,
+ *        their lse too.
  * A token that a row does not see has no part in it, whatever its K and V
  * hold (NaN and infinities too).
  */
 pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
                          const int32_t *table, const int32_t *start, const int32_t *count,
                          const uint32_t *mask, void *out, float *lse, int hq, int tree,
-                         pbs_cache c, float scale, int dtype, void *ws, size_t ws_bytes,
-                         pbs_stream_t st);
+                         pbs_cache c, float scale, int zero_rest, int dtype, void *ws,
+                         size_t ws_bytes, pbs_stream_t st);
 
 /* Bytes of device workspace pbs_tree_attn needs (0 for a refused shape); they
  * depend on the device's SM count, hq, tree and c, not on the lengths. */

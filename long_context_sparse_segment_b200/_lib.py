@@ -83,7 +83,7 @@ _SIGS = {
     "pbs_cache_compact": (_i, [_vp] * 6 + [Cache, _vp, _sz, _vp]),
     "pbs_cache_accept": (_i, [_vp] * 7 + [_i, Cache, _vp]),
     "pbs_tree_mask": (_i, [_vp, _vp, _vp, _i, _i, _vp]),
-    "pbs_tree_attn": (_i, [Rows] + [_vp] * 8 + [_i, _i, Cache, _f, _i, _vp, _sz, _vp]),
+    "pbs_tree_attn": (_i, [Rows] + [_vp] * 8 + [_i, _i, Cache, _f, _i, _i, _vp, _sz, _vp]),
     "pbs_tree_workspace_bytes": (_sz, [_i, _i, Cache]),
     "pbs_get_device_status": (_i, [_vp, ctypes.POINTER(_i), ctypes.POINTER(_i)]),
     "pbs_status_string": (ctypes.c_char_p, [_i]),

@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libpbs.so")
 
 SOURCES = ["api.cu", "score.cu", "score_static.cu", "permute.cu", "select.cu", "attn_mma.cu", "attn_tc.cu",
            "score_tc.cu", "tmap.cu", "attn_tc2.cu", "attn_tc64.cu",
-           "mass_tc.cu", "rope.cu", "cache.cu", "tree.cu"]
+           "mass_tc.cu", "rope.cu", "cache.cu", "tree.cu", "tree_tc.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pbs.h"
 
 namespace pbs {
@@ -17,6 +19,23 @@ inline bool rows_ok(const pbs_rows &r, int elem) {
   const int64_t v = 16 / elem;
   return r.p && ((uintptr_t)r.p & 15u) == 0 && r.layer % v == 0 && r.batch % v == 0 &&
          r.head % v == 0 && r.row % v == 0;
+}
+
+// SMs of the current device, looked up once per device.
+int sm_count_cached();
+
+// The dynamic shared memory of a kernel allowed once per device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit & done.load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

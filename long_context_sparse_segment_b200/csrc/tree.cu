@@ -8,250 +8,17 @@
 // once per item and serves them all. With few rows this is bound by reading
 // the cache.
 //
-// Work. The key tiles of all items (sequence, KV head, tile of rows) form
-// one line of units, cut into equal runs, one per CTA (one CTA per SM): a
-// ragged batch and a single long sequence load every SM alike, and the
-// lengths are read on the device. A run that holds all of an item's units
-// writes its rows; an item cut by a run's end leaves its running maximum,
-// sum and output (fp32) in the workspace, at most two per CTA, and the
-// combining kernel joins them in unit order, so results do not depend on
-// timing.
-//
 // This kernel: up to 32 rows an item, warp MMA. Eight warps take tiles of 64
 // keys, four warps a tile (16 keys each) and the two halves in turn, each
 // with its own maximum, sum and output, joined when the item ends; a ninth
 // warp brings the tiles by TMA, page by page, into a ring.
-#include <cuda.h>
-#include <cuda_fp16.h>
-
-#include "common.cuh"
-#include "decode.h"
 #include "internal.h"
-#include "tc.cuh"
+#include "tree_tc.h"
 
 namespace pbs {
 namespace {
 
-using namespace tc;
-
-constexpr int kMaxSeqs = 2048;   // the units before each sequence stay in shared memory
-constexpr int kMaxTree = 1024;   // 32 mask words a row
-
-struct TreeArgs {
-  pbs_rows q;
-  const int32_t *table, *start, *count;
-  const uint32_t *mask;
-  const void *v_pages;  // for the non-finite rows of drafts
-  void *out;
-  float *lse;
-  float *part_o;    // [2 grid][rows][d]
-  float2 *part_ml;  // [2 grid][rows]: running maximum (log2) and sum
-  int *part_bad;    // [2 grid]: drafted V rows with NaN or infinity met
-  int *err;
-  int hq, hkv, G, tree, words, seqs, width, page, pages;
-  float sl2;
-};
-
-// What a sequence asks for: its cached tokens and drafts (0 where the call
-// has to leave it alone).
-struct Seq {
-  int start, count;
-};
-
-__device__ __forceinline__ Seq seq_of(const TreeArgs &a, int s) {
-  Seq q{__ldg(a.start + s), a.count ? min(__ldg(a.count + s), a.tree) : a.tree};
-  if (q.count <= 0) return {0, 0};
-  if (q.start < 0 || (int64_t)q.start + q.count > (int64_t)a.width * a.page) {
-    report(a.err, PBS_ERR_DEVICE_ASSERT);
-    return {0, 0};
-  }
-  return q;
-}
-
-__device__ __forceinline__ int cdiv(int x, int y) { return (x + y - 1) / y; }
-
-// Units of a sequence: its items (KV head, row tile) times its key tiles.
-template <int ROWS, int KEYS>
-__device__ __forceinline__ int units_of(const TreeArgs &a, const Seq &q) {
-  return q.count ? a.hkv * cdiv(q.count * a.G, ROWS) * cdiv(q.start + q.count, KEYS) : 0;
-}
-
-// Inclusive sums over a block of NT threads (a multiple of 32).
-template <int NT>
-__device__ __forceinline__ int block_scan(int x, int *sh) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  int add = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) add += w < warp ? sh[w] : 0;
-  __syncthreads();
-  return x + add;
-}
-
-// before[s]: units of the sequences in front of s; before[seqs]: all.
-template <int ROWS, int KEYS, int NT>
-__device__ __forceinline__ void plan_units(const TreeArgs &a, int *before, int *sh) {
-  int base = 0;
-  for (int s0 = 0; s0 < a.seqs; s0 += NT) {
-    const int s = s0 + threadIdx.x;
-    const int x = s < a.seqs ? units_of<ROWS, KEYS>(a, seq_of(a, s)) : 0;
-    const int inc = block_scan<NT>(x, sh);
-    if (s < a.seqs) before[s] = base + inc - x;
-    if (threadIdx.x == NT - 1) sh[NT / 32] = inc;
-    __syncthreads();
-    base += sh[NT / 32];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) before[a.seqs] = base;
-  __syncthreads();
-}
-
-// The units of CTA c: [run_start(c), run_start(c + 1)); none is empty with
-// runs = min(total, CTAs) of them. The run that unit u belongs to.
-__device__ __forceinline__ int run_start(int total, int c, int runs) {
-  return (int)((int64_t)total * c / runs);
-}
-__device__ __forceinline__ int run_owner(int total, int u, int runs) {
-  return (int)((((int64_t)u + 1) * runs - 1) / total);
-}
-
-// A piece of a CTA's run inside one item.
-struct Segment {
-  int s, h, rt;      // sequence, KV head, row tile
-  int start, count;  // tokens, drafts
-  int k0, k1;        // key tiles
-  int whole;         // all of the item's key tiles
-};
-
-template <int ROWS, int KEYS>
-__device__ __forceinline__ Segment segment_at(const TreeArgs &a, const int *before, int u, int end,
-                                              int *s_hint) {
-  int s = *s_hint;
-  while (before[s + 1] <= u) ++s;
-  *s_hint = s;
-  const Seq q = seq_of(a, s);
-  const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(q.count * a.G, ROWS);
-  const int x = u - before[s], item = x / kt;
-  Segment g;
-  g.s = s, g.h = item / rts, g.rt = item % rts;
-  g.start = q.start, g.count = q.count;
-  g.k0 = x - item * kt;
-  g.k1 = min(kt, g.k0 + end - u);
-  g.whole = g.k1 - g.k0 == kt;
-  return g;
-}
-
-// Whether draft i sees draft j (j < count).
-__device__ __forceinline__ bool sees(const TreeArgs &a, int s, int i, int j) {
-  if (!a.mask) return j <= i;
-  return __ldg(a.mask + ((size_t)s * a.tree + i) * a.words + (j >> 5)) >> (j & 31) & 1;
-}
-
-// ---------------------------------------------------------------- 16-bit types
-template <typename T>
-struct Two;
-template <>
-struct Two<__nv_bfloat16> {
-  static __device__ __forceinline__ uint32_t pack(float x, float y) { return pack_bf16(x, y); }
-  static __device__ __forceinline__ float2 unpack(uint32_t u) {
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-  }
-  static constexpr uint32_t kExp = 0x7f80u;
-  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                             uint32_t b1) {
-    mma_16816(c, a, b0, b1);
-  }
-};
-template <>
-struct Two<__half> {
-  static __device__ __forceinline__ uint32_t pack(float x, float y) {
-    const __half2 v = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t *>(&v);
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t u) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
-  }
-  static constexpr uint32_t kExp = 0x7c00u;
-  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                             uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
-        "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-};
-
-// NaN or infinity in a 16-bit value.
-template <typename T>
-__device__ __forceinline__ bool wild16(uint32_t x) {
-  return (x & Two<T>::kExp) == Two<T>::kExp;
-}
-
-// The two halves of u that `keep` (bits 0, 1) has; with `drafted` (bits 0, 1)
-// a NaN or infinity in such a half becomes 0 and *bad is set.
-template <typename T>
-__device__ __forceinline__ uint32_t clean2(uint32_t u, unsigned keep, unsigned drafted, bool *bad) {
-  uint32_t lo = keep & 1 ? u & 0xffffu : 0, hi = keep & 2 ? u & 0xffff0000u : 0;
-  if ((drafted & 1) && wild16<T>(lo)) lo = 0, *bad = true;
-  if ((drafted & 2) && wild16<T>(hi >> 16)) hi = 0, *bad = true;
-  return lo | hi;
-}
-
-// The product P V leaves NaN and infinite values of drafted V rows out, since
-// 0 times them would reach the rows that do not see them. This adds them to a
-// row that does: columns [col, col + N) of draft i's output.
-template <typename T, int N>
-__device__ __noinline__ void add_wild(const TreeArgs &a, int s, int h, const Seq &q, int i,
-                                      int d, int col, float (&o)[N]) {
-  for (int j = 0; j < q.count; ++j) {
-    if (!sees(a, s, i, j)) continue;
-    const int t = q.start + j;
-    const int page = __ldg(a.table + (size_t)s * a.width + t / a.page);
-    if (page < 0 || page >= a.pages) continue;
-    const T *v = (const T *)a.v_pages +
-                 (((size_t)page * a.hkv + h) * a.page + t % a.page) * d + col;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float x = (float)v[e];
-      if (!isfinite(x)) o[e] += x;
-    }
-  }
-}
-
-// N output columns of row r of an item, from fp32.
-template <typename T, int N>
-__device__ __forceinline__ void write_row(const TreeArgs &a, int s, int h, int r, int d, int col,
-                                          const float (&o)[N]) {
-  const int i = r / a.G, g = r % a.G;
-  T *dst = (T *)a.out + (((size_t)s * a.hq + h * a.G + g) * a.tree + i) * d + col;
-  uint32_t p[N / 2];
-#pragma unroll
-  for (int e = 0; e < N / 2; ++e) p[e] = Two<T>::pack(o[2 * e], o[2 * e + 1]);
-  if constexpr (N == 8)
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(p[0], p[1], p[2], p[3]);
-  else if constexpr (N == 4)
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(p[0], p[1]);
-  else
-    *reinterpret_cast<uint32_t *>(dst) = p[0];
-}
-
-__device__ __forceinline__ void write_lse(const TreeArgs &a, int s, int h, int r, float m, float l) {
-  if (a.lse)
-    a.lse[((size_t)s * a.hq + h * a.G + r % a.G) * a.tree + r / a.G] =
-        l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
-// 2^(m - top) for a part whose maximum is m, top the maximum of all parts.
-__device__ __forceinline__ float part_scale(float m, float top) {
-  return m == top ? 1.f : ex2_approx(m - top);
-}
+using namespace tree;
 
 // ------------------------------------------------------------- warp-MMA kernel
 constexpr int kKeys = 64;       // keys of a unit
@@ -269,9 +36,8 @@ struct MmaCfg {
   struct Bars {
     uint64_t full[ST], empty[ST], join;
     int abort, bad;
-    int sh[12];
     float2 ml[kConsumers][ROWS];
-    int before[kMaxSeqs + 1];
+    Place place;
   };
   static constexpr size_t SMEM = 1024 + 2 * KV * ST + ROWS * D * 2 + JOIN + sizeof(Bars);
 };
@@ -298,13 +64,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     bar->abort = 0, bar->bad = 0;
     fence_barrier_init();
   }
-  plan_units<ROWS, kKeys, kMmaThreads>(a, bar->before, bar->sh);
-  const int *before = bar->before;
-  const int total = before[a.seqs];
-  const int runs = min(total, (int)gridDim.x);
-  if ((int)blockIdx.x >= runs) return;
-  const int u0 = run_start(total, blockIdx.x, runs);
-  const int u1 = run_start(total, blockIdx.x + 1, runs);
+  if (!find_place<ROWS, kKeys, kMmaThreads>(a, &bar->place)) return;
+  Walk<ROWS, kKeys> walk(bar->place);
+  Segment g;
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------- producer
@@ -314,11 +76,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     const int box = min(a.page, kKeys), pieces = kKeys / box;
     const int kv = lane & 1, half = (lane >> 1) % H, piece = (lane >> 1) / H;
     const bool mine = piece < pieces;
-    int hint = 0, it = 0;
+    int it = 0;
     bool ok = true;
     if (lane == 0) prefetch_map(&tmK), prefetch_map(&tmV);
-    for (int u = u0; u < u1 && ok;) {
-      const Segment g = segment_at<ROWS, kKeys>(a, before, u, u1, &hint);
+    while (ok && walk.next(a, &g)) {
       const int len = g.start + g.count;
       const int32_t *row = a.table + (size_t)g.s * a.width;
       for (int k = g.k0; k < g.k1; ++k, ++it) {
@@ -347,7 +108,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                       kv ? &tmV : &tmK, &bar->full[st], half * 64, y);
         __syncwarp();
       }
-      u += g.k1 - g.k0;
     }
     // every copy started here lands before the CTA exits
     int never = 0;
@@ -366,9 +126,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     phase ^= 1;
     return ok;
   };
-  int hint = 0, it = 0;
-  for (int u = u0; u < u1;) {
-    const Segment g = segment_at<ROWS, kKeys>(a, before, u, u1, &hint);
+  int it = 0;
+  for (int seg = 0; walk.next(a, &g); ++seg) {
     const int rows = min(ROWS, g.count * a.G - g.rt * ROWS);  // of this row tile
     const int len = g.start + g.count;
     // Q rows into shared memory, 16-byte chunks XOR-swizzled by row
@@ -438,13 +197,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t seen = seen_word(a, g, draft[mt][x], key0) >> qc;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int j = key0 + n * 8 + qc + (e & 1) - g.start;
-                if (j >= 0 && (j >= g.count || !sees(a, g.s, draft[mt][e >> 1], j)))
-                  s[mt][n][e] = -INFINITY;
-              }
+              for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (!(seen >> (n * 8 + e) & 1)) s[mt][n][2 * x + e] = -INFINITY;
+            }
         }
         // running maximum, P in two 16-bit parts: 16 bits alone would add as
         // much error as the output's own rounding
@@ -526,7 +286,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         t += __shfl_xor_sync(0xffffffffu, t, 2);
         if ((lane & 3) == 0) bar->ml[warp][mt * 16 + gr + 8 * x] = make_float2(m[mt][x], t);
       }
-    const int slot = 2 * blockIdx.x + (u != u0);
+    const int slot = 2 * blockIdx.x + (seg > 0);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (mt * 16 < rows) {
@@ -582,77 +342,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       }
       if (!sync()) return;  // the join buffer and Q are free again
     }
-    u += g.k1 - g.k0;
   }
-}
-
-// -------------------------------------------------------------------- combine
-// One warp per row of an item that several CTAs worked on: their parts, in
-// order, scaled to the common maximum. Bound by latency: a part is read once.
-constexpr int kCombineThreads = 128;
-
-template <typename T, int D, int ROWS, int KEYS>
-__global__ void __launch_bounds__(kCombineThreads)
-    tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
-  __shared__ int sh[8];
-  const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Seq q = seq_of(a, s);
-  if (blockIdx.x * 4 >= q.count * a.G) return;
-  // units before this sequence, and all
-  int mine = 0, all = 0;
-  for (int i = tid; i < a.seqs; i += kCombineThreads) {
-    const int x = units_of<ROWS, KEYS>(a, seq_of(a, i));
-    all += x;
-    if (i < s) mine += x;
-  }
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  all = __reduce_add_sync(0xffffffffu, all);
-  if (lane == 0) sh[warp] = mine, sh[4 + warp] = all;
-  __syncthreads();
-  const int r = blockIdx.x * 4 + warp;  // row of the (sequence, KV head)
-  if (r >= q.count * a.G) return;
-  const int total = sh[4] + sh[5] + sh[6] + sh[7], runs = min(total, grid);
-  const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(q.count * a.G, ROWS);
-  const int u0 = sh[0] + sh[1] + sh[2] + sh[3] + (h * rts + r / ROWS) * kt;
-  const int c0 = run_owner(total, u0, runs), c1 = run_owner(total, u0 + kt - 1, runs);
-  if (c0 == c1) return;
-  const int slot0 = 2 * c0 + (run_start(total, c0, runs) != u0);
-  auto slot = [&](int c) { return c == c0 ? slot0 : 2 * c; };
-  const int rr = r % ROWS;
-  float top = -INFINITY;
-  int bad = 0;
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    top = fmaxf(top, a.part_ml[(size_t)slot(c) * ROWS + rr].x);
-    bad |= a.part_bad[slot(c)];
-  }
-  top = warp_max(top);
-  bad = __any_sync(0xffffffffu, bad);
-  constexpr int N = D / 32;
-  const int col = lane * N;
-  float acc[N], sum = 0.f;
-#pragma unroll
-  for (int e = 0; e < N; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const size_t at = (size_t)slot(c) * ROWS + rr;
-    const float2 ml = a.part_ml[at];
-    const float f = part_scale(ml.x, top);
-    sum += ml.y * f;
-    const float *src = a.part_o + at * D + col;
-    if constexpr (N == 4) {
-      const float4 v = *reinterpret_cast<const float4 *>(src);
-      acc[0] += v.x * f, acc[1] += v.y * f, acc[2] += v.z * f, acc[3] += v.w * f;
-    } else {
-      const float2 v = *reinterpret_cast<const float2 *>(src);
-      acc[0] += v.x * f, acc[1] += v.y * f;
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int e = 0; e < N; ++e) acc[e] *= inv;
-  if (bad) add_wild<T, N>(a, s, h, q, r / a.G, D, col, acc);
-  write_row<T, N>(a, s, h, r, D, col, acc);
-  if (lane == 0) write_lse(a, s, h, r, top, sum);
 }
 
 // ----------------------------------------------------------------- tree masks
@@ -682,6 +372,19 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ host side
+}  // namespace
+
+int sm_count_cached() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count();
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (!n) known[dev].store(n = sm_count(), std::memory_order_relaxed);
+  return n;
+}
+
+namespace {
+
 bool tree_shape_ok(int hq, int tree, const pbs_cache &c) {
   return hq >= 1 && c.hkv >= 1 && hq % c.hkv == 0 && tree >= 0 && c.seqs >= 0 && c.pages >= 1 &&
          c.page >= 1 && c.width >= 1;
@@ -690,7 +393,7 @@ bool tree_shape_ok(int hq, int tree, const pbs_cache &c) {
 // What the kernels take, beyond what makes sense.
 bool tree_supported(int hq, int tree, const pbs_cache &c) {
   if ((c.d != 64 && c.d != 128) || c.page < 16 || c.page > 256 || (c.page & (c.page - 1)) ||
-      tree > kMaxTree || c.seqs > kMaxSeqs || hq > 65536 || c.hkv > 65535 ||
+      tree > kMaxTree || c.seqs > 65535 || hq > 65536 || c.hkv > 65535 ||
       (int64_t)c.pages * c.hkv * c.page >= (1ll << 31) ||
       (int64_t)c.width * c.page >= (1ll << 31) - 2 * kMaxTree)
     return false;
@@ -701,14 +404,15 @@ bool tree_supported(int hq, int tree, const pbs_cache &c) {
 }
 
 int row_tile(int hq, int tree, const pbs_cache &c) {
-  return (int64_t)(hq / c.hkv) * tree <= 16 ? 16 : 32;
+  const int64_t rows = (int64_t)(hq / c.hkv) * tree;
+  return rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
 }
 
 struct Parts {
   size_t o, ml, bad, bytes;
 };
 Parts parts(int rows, int d) {
-  const size_t slots = 2 * (size_t)sm_count();
+  const size_t slots = 2 * (size_t)sm_count_cached();
   Parts p;
   p.o = 0;
   p.ml = slots * rows * d * 4;
@@ -718,26 +422,14 @@ Parts parts(int rows, int d) {
 }
 
 template <typename T, int D, int MT>
-cudaError_t run_mma(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a,
+cudaError_t run_mma(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int grid,
                     cudaStream_t st) {
   using C = MmaCfg<D, MT>;
-  auto kern = tree_mma_kernel<T, D, MT>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  constexpr auto kern = tree_mma_kernel<T, D, MT>;
+  const cudaError_t e = allow_smem<kern>((int)C::SMEM);
   if (e != cudaSuccess) return e;
-  const int grid = sm_count();
   kern<<<grid, kMmaThreads, C::SMEM, st>>>(mk, mv, a);
-  const dim3 cg((unsigned)ceil_div((int64_t)a.G * a.tree, 4), a.hkv, a.seqs);
-  tree_combine_kernel<T, D, C::ROWS, kKeys><<<cg, kCombineThreads, 0, st>>>(a, grid);
-  return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t run_tree(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int d,
-                     int rows, cudaStream_t st) {
-  if (d == 64)
-    return rows == 16 ? run_mma<T, 64, 1>(mk, mv, a, st) : run_mma<T, 64, 2>(mk, mv, a, st);
-  return rows == 16 ? run_mma<T, 128, 1>(mk, mv, a, st) : run_mma<T, 128, 2>(mk, mv, a, st);
+  return launch_combine<T, D, C::ROWS, kKeys>(a, grid, st);
 }
 
 }  // namespace
@@ -769,8 +461,8 @@ size_t pbs_tree_workspace_bytes(int hq, int tree, pbs_cache c) {
 pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
                          const int32_t *table, const int32_t *start, const int32_t *count,
                          const uint32_t *mask, void *out, float *lse, int hq, int tree,
-                         pbs_cache c, float scale, int dtype, void *ws, size_t ws_bytes,
-                         pbs_stream_t st) {
+                         pbs_cache c, float scale, int zero_rest, int dtype, void *ws,
+                         size_t ws_bytes, pbs_stream_t st) {
   if (!tree_shape_ok(hq, tree, c) || (dtype != PBS_BF16 && dtype != PBS_FP16))
     return PBS_ERR_INVALID_ARG;
   if (!tree_supported(hq, tree, c)) return PBS_ERR_UNSUPPORTED;
@@ -794,14 +486,24 @@ pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
   a.seqs = c.seqs, a.width = c.width, a.page = c.page, a.pages = c.pages;
   const float sigma = scale > 0.f ? scale : (float)(1.0 / sqrt((double)c.d));
   a.sl2 = sigma * kLog2e;
+  a.zero_rest = zero_rest != 0;
   CUtensorMap mk, mv;
   const uint64_t all = (uint64_t)c.pages * c.hkv * c.page;
-  const int box = c.page < kKeys ? c.page : kKeys;
+  const int keys = rows == 16 ? kKeys : 128, box = c.page < keys ? c.page : keys;
   if (!make_tile_map(&mk, k_pages, all, c.d, box) || !make_tile_map(&mv, v_pages, all, c.d, box))
     return PBS_ERR_CUDA;
   cudaStream_t cs = (cudaStream_t)st;
-  const cudaError_t e = dtype == PBS_BF16 ? run_tree<__nv_bfloat16>(mk, mv, a, c.d, rows, cs)
-                                          : run_tree<__half>(mk, mv, a, c.d, rows, cs);
+  const int grid = sm_count_cached();
+  const bool bf16 = dtype == PBS_BF16;
+  cudaError_t e;
+  if (rows > 16)
+    e = launch_tree_tc(mk, mv, a, c.d, rows, bf16, grid, cs);
+  else if (c.d == 64)
+    e = bf16 ? run_mma<__nv_bfloat16, 64, 1>(mk, mv, a, grid, cs)
+             : run_mma<__half, 64, 1>(mk, mv, a, grid, cs);
+  else
+    e = bf16 ? run_mma<__nv_bfloat16, 128, 1>(mk, mv, a, grid, cs)
+             : run_mma<__half, 128, 1>(mk, mv, a, grid, cs);
   return e == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
 }
 

@@ -1,0 +1,376 @@
+// Shared by the kernels of pbs_tree_attn: what a call asks for, how its work
+// is cut into runs, the types, and the kernel that joins the parts.
+//
+// Work. The key tiles of all items (sequence, KV head, tile of rows) form
+// one line of units, cut into equal runs, one per CTA (one CTA per SM): a
+// ragged batch and a single long sequence load every SM alike, and the
+// lengths are read on the device. A run that holds all of an item's units
+// writes its rows; an item cut by a run's end leaves its running maximum,
+// sum and output (fp32) in the workspace, at most two per CTA, and the
+// combining kernel joins them in unit order, so results do not depend on
+// timing.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "decode.h"
+#include "tc.cuh"
+
+namespace pbs {
+namespace tree {
+
+using namespace tc;
+
+constexpr int kMaxTree = 1024;   // 32 mask words a row
+
+struct TreeArgs {
+  pbs_rows q;
+  const int32_t *table, *start, *count;
+  const uint32_t *mask;
+  const void *v_pages;  // for the non-finite rows of drafts
+  void *out;
+  float *lse;
+  float *part_o;    // [2 grid][rows][d]
+  float2 *part_ml;  // [2 grid][rows]: running maximum (log2) and sum
+  int *part_bad;    // [2 grid]: drafted V rows with NaN or infinity met
+  int *err;
+  int hq, hkv, G, tree, words, seqs, width, page, pages;
+  int zero_rest;  // rows behind a sequence's count become 0 instead of staying
+  float sl2;
+};
+
+// What a sequence asks for: its cached tokens and drafts (0 where the call
+// has to leave it alone).
+struct Seq {
+  int start, count;
+};
+
+__device__ __forceinline__ Seq seq_of(const TreeArgs &a, int s) {
+  Seq q{__ldg(a.start + s), a.count ? min(__ldg(a.count + s), a.tree) : a.tree};
+  if (q.count <= 0) return {0, 0};
+  if (q.start < 0 || (int64_t)q.start + q.count > (int64_t)a.width * a.page) {
+    report(a.err, PBS_ERR_DEVICE_ASSERT);
+    return {0, 0};
+  }
+  return q;
+}
+
+__device__ __forceinline__ int cdiv(int x, int y) { return (x + y - 1) / y; }
+
+// Units of a sequence: its items (KV head, row tile) times its key tiles.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ int units_of(const TreeArgs &a, const Seq &q) {
+  return q.count ? a.hkv * cdiv(q.count * a.G, ROWS) * cdiv(q.start + q.count, KEYS) : 0;
+}
+
+// The units of CTA c: [start(c), start(c + 1)); none is empty with
+// runs = min(total, CTAs) of them, the first `extra` one unit longer. The run
+// that unit u belongs to.
+struct Runs {
+  int base, extra;
+  __device__ __forceinline__ Runs(int total, int runs)
+      : base(total / runs), extra(total - total / runs * runs) {}
+  __device__ __forceinline__ int start(int c) const { return c * base + min(c, extra); }
+  __device__ __forceinline__ int owner(int u) const {
+    const int cut = extra * (base + 1);
+    return u < cut ? u / (base + 1) : extra + (u - cut) / base;
+  }
+};
+
+// The place of a CTA's run: its first and end unit, and the sequence that the
+// first lies in with the units before that one. Filled once per CTA.
+struct Place {
+  int u0, u1, s, before;
+  int sum[17];
+};
+
+// Every thread of the block (NT of them, a multiple of 32) calls it; false
+// for a CTA without units.
+template <int ROWS, int KEYS, int NT>
+__device__ __forceinline__ bool find_place(const TreeArgs &a, Place *p) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto units = [&](int s) { return s < a.seqs ? units_of<ROWS, KEYS>(a, seq_of(a, s)) : 0; };
+  int sum = 0;
+  for (int s = tid; s < a.seqs; s += NT) sum += units(s);
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (lane == 0) p->sum[warp] = sum;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) total += p->sum[w];
+  const int runs = min(total, (int)gridDim.x);
+  if ((int)blockIdx.x >= runs) return false;
+  const Runs run(total, runs);
+  const int u0 = run.start(blockIdx.x);
+  if (warp == 0) {
+    int base = 0;
+    for (int s0 = 0;; s0 += 32) {
+      const int x = units(s0 + lane);
+      int inc = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      inc += base;
+      const unsigned m = __ballot_sync(0xffffffffu, inc > u0);
+      if (m) {
+        if (lane == __ffs(m) - 1) {
+          p->u0 = u0, p->u1 = run.start(blockIdx.x + 1);
+          p->s = s0 + lane, p->before = inc - x;
+        }
+        break;
+      }
+      base = __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  __syncthreads();
+  return true;
+}
+
+// A piece of a CTA's run inside one item.
+struct Segment {
+  int s, h, rt;      // sequence, KV head, row tile
+  int start, count;  // tokens, drafts
+  int k0, k1;        // key tiles
+  int whole;         // all of the item's key tiles
+};
+
+// The segments of a run, one after the other.
+template <int ROWS, int KEYS>
+struct Walk {
+  int u, u1, s, before;
+  __device__ __forceinline__ explicit Walk(const Place &p)
+      : u(p.u0), u1(p.u1), s(p.s), before(p.before) {}
+  __device__ __forceinline__ bool next(const TreeArgs &a, Segment *g) {
+    if (u >= u1) return false;
+    Seq q = seq_of(a, s);
+    for (int n; u >= before + (n = units_of<ROWS, KEYS>(a, q));) {
+      before += n;
+      q = seq_of(a, ++s);
+    }
+    const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(q.count * a.G, ROWS);
+    const int x = u - before, item = x / kt;
+    g->s = s, g->h = item / rts, g->rt = item - g->h * rts;
+    g->start = q.start, g->count = q.count;
+    g->k0 = x - item * kt;
+    g->k1 = min(kt, g->k0 + u1 - u);
+    g->whole = g->k1 - g->k0 == kt;
+    u += g->k1 - g->k0;
+    return true;
+  }
+};
+
+// Whether draft i sees draft j (j < count).
+__device__ __forceinline__ bool sees(const TreeArgs &a, int s, int i, int j) {
+  if (!a.mask) return j <= i;
+  return __ldg(a.mask + ((size_t)s * a.tree + i) * a.words + (j >> 5)) >> (j & 31) & 1;
+}
+
+// Bit x of the result: whether draft i of sequence s sees key `key` + x, given
+// that some of the 32 keys are drafts or lie behind the last token.
+__device__ __forceinline__ uint32_t seen_word(const TreeArgs &a, const Segment &g, int i, int key) {
+  const int j = key - g.start, left = g.count - j;  // drafts from the first key on
+  if (left <= 0) return 0;
+  auto word = [&](int w) -> uint32_t {
+    if (w < 0) return 0xffffffffu;  // the prefix
+    if (w >= a.words) return 0;
+    if (a.mask) return __ldg(a.mask + ((size_t)g.s * a.tree + i) * a.words + w);
+    return w < i >> 5 ? 0xffffffffu : w > i >> 5 ? 0u : (2u << (i & 31)) - 1;
+  };
+  const int w = j >> 5;
+  uint32_t x = word(w);
+  if (j & 31) x = __funnelshift_r(x, word(w + 1), j & 31);
+  return left < 32 ? x & ((1u << left) - 1) : x;
+}
+
+// ---------------------------------------------------------------- 16-bit types
+template <typename T>
+struct Two;
+template <>
+struct Two<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t pack(float x, float y) { return pack_bf16(x, y); }
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  static constexpr uint32_t kExp = 0x7f80u;
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+    mma_16816(c, a, b0, b1);
+  }
+};
+template <>
+struct Two<__half> {
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+  }
+  static constexpr uint32_t kExp = 0x7c00u;
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+        "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+
+// NaN or infinity in a 16-bit value.
+template <typename T>
+__device__ __forceinline__ bool wild16(uint32_t x) {
+  return (x & Two<T>::kExp) == Two<T>::kExp;
+}
+
+// The two halves of u that `keep` (bits 0, 1) has; with `drafted` (bits 0, 1)
+// a NaN or infinity in such a half becomes 0 and *bad is set.
+template <typename T>
+__device__ __forceinline__ uint32_t clean2(uint32_t u, unsigned keep, unsigned drafted, bool *bad) {
+  uint32_t lo = keep & 1 ? u & 0xffffu : 0, hi = keep & 2 ? u & 0xffff0000u : 0;
+  if ((drafted & 1) && wild16<T>(lo)) lo = 0, *bad = true;
+  if ((drafted & 2) && wild16<T>(hi >> 16)) hi = 0, *bad = true;
+  return lo | hi;
+}
+
+// The product P V leaves NaN and infinite values of drafted V rows out, since
+// 0 times them would reach the rows that do not see them. This adds them to a
+// row that does: columns [col, col + N) of draft i's output.
+template <typename T, int N>
+__device__ __noinline__ void add_wild(const TreeArgs &a, int s, int h, const Seq &q, int i,
+                                      int d, int col, float (&o)[N]) {
+  for (int j = 0; j < q.count; ++j) {
+    if (!sees(a, s, i, j)) continue;
+    const int t = q.start + j;
+    const int page = __ldg(a.table + (size_t)s * a.width + t / a.page);
+    if (page < 0 || page >= a.pages) continue;
+    const T *v = (const T *)a.v_pages +
+                 (((size_t)page * a.hkv + h) * a.page + t % a.page) * d + col;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float x = (float)v[e];
+      if (!isfinite(x)) o[e] += x;
+    }
+  }
+}
+
+// N output columns of row r of an item, from fp32.
+template <typename T, int N>
+__device__ __forceinline__ void write_row(const TreeArgs &a, int s, int h, int r, int d, int col,
+                                          const float (&o)[N]) {
+  const int i = r / a.G, g = r % a.G;
+  T *dst = (T *)a.out + (((size_t)s * a.hq + h * a.G + g) * a.tree + i) * d + col;
+  uint32_t p[N / 2];
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) p[e] = Two<T>::pack(o[2 * e], o[2 * e + 1]);
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(p[0], p[1], p[2], p[3]);
+  else if constexpr (N == 4)
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(p[0], p[1]);
+  else
+    *reinterpret_cast<uint32_t *>(dst) = p[0];
+}
+
+__device__ __forceinline__ void write_lse(const TreeArgs &a, int s, int h, int r, float m, float l) {
+  if (a.lse)
+    a.lse[((size_t)s * a.hq + h * a.G + r % a.G) * a.tree + r / a.G] =
+        l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// 2^(m - top) for a part whose maximum is m, top the maximum of all parts.
+__device__ __forceinline__ float part_scale(float m, float top) {
+  return m == top ? 1.f : ex2_approx(m - top);
+}
+
+// -------------------------------------------------------------------- combine
+// One warp per row of an item that several CTAs worked on: their parts, in
+// order, scaled to the common maximum. Bound by latency: a part is read once.
+constexpr int kCombineThreads = 128;
+
+template <typename T, int D, int ROWS, int KEYS>
+__global__ void __launch_bounds__(kCombineThreads)
+    tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
+  __shared__ int sh[8];
+  const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Seq q = seq_of(a, s);
+  if (a.zero_rest) {
+    const int r = blockIdx.x * 4 + warp;
+    if (r >= q.count * a.G && r < a.tree * a.G) {
+      constexpr int N = D / 32;
+      const float o[N] = {};
+      write_row<T, N>(a, s, h, r, D, lane * N, o);
+      if (lane == 0 && a.lse) a.lse[((size_t)s * a.hq + h * a.G + r % a.G) * a.tree + r / a.G] = 0.f;
+    }
+  }
+  if (blockIdx.x * 4 >= q.count * a.G) return;
+  // units before this sequence, and all
+  int mine = 0, all = 0;
+  for (int i = tid; i < a.seqs; i += kCombineThreads) {
+    const int x = units_of<ROWS, KEYS>(a, seq_of(a, i));
+    all += x;
+    if (i < s) mine += x;
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (lane == 0) sh[warp] = mine, sh[4 + warp] = all;
+  __syncthreads();
+  const int r = blockIdx.x * 4 + warp;  // row of the (sequence, KV head)
+  if (r >= q.count * a.G) return;
+  const int total = sh[4] + sh[5] + sh[6] + sh[7], runs = min(total, grid);
+  const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(q.count * a.G, ROWS);
+  const int u0 = sh[0] + sh[1] + sh[2] + sh[3] + (h * rts + r / ROWS) * kt;
+  const Runs run(total, runs);
+  const int c0 = run.owner(u0), c1 = run.owner(u0 + kt - 1);
+  if (c0 == c1) return;
+  const int slot0 = 2 * c0 + (run.start(c0) != u0);
+  auto slot = [&](int c) { return c == c0 ? slot0 : 2 * c; };
+  const int rr = r % ROWS;
+  float top = -INFINITY;
+  int bad = 0;
+  for (int c = c0 + lane; c <= c1; c += 32) {
+    top = fmaxf(top, a.part_ml[(size_t)slot(c) * ROWS + rr].x);
+    bad |= a.part_bad[slot(c)];
+  }
+  top = warp_max(top);
+  bad = __any_sync(0xffffffffu, bad);
+  constexpr int N = D / 32;
+  const int col = lane * N;
+  float acc[N], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const size_t at = (size_t)slot(c) * ROWS + rr;
+    const float2 ml = a.part_ml[at];
+    const float f = part_scale(ml.x, top);
+    sum += ml.y * f;
+    const float *src = a.part_o + at * D + col;
+    if constexpr (N == 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(src);
+      acc[0] += v.x * f, acc[1] += v.y * f, acc[2] += v.z * f, acc[3] += v.w * f;
+    } else {
+      const float2 v = *reinterpret_cast<const float2 *>(src);
+      acc[0] += v.x * f, acc[1] += v.y * f;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] *= inv;
+  if (bad) add_wild<T, N>(a, s, h, q, r / a.G, D, col, acc);
+  write_row<T, N>(a, s, h, r, D, col, acc);
+  if (lane == 0) write_lse(a, s, h, r, top, sum);
+}
+
+template <typename T, int D, int ROWS, int KEYS>
+cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
+  const dim3 blocks((unsigned)ceil_div((int64_t)a.G * a.tree, 4), a.hkv, a.seqs);
+  tree_combine_kernel<T, D, ROWS, KEYS><<<blocks, kCombineThreads, 0, st>>>(a, grid);
+  return cudaGetLastError();
+}
+
+}  // namespace tree
+}  // namespace pbs

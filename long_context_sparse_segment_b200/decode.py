@@ -16,8 +16,7 @@ import math
 import torch
 
 from . import _lib
-from ._lib import Cache, Rows, lib
-from .ops import _call, _ptr, _stream
+from ._lib import Cache, Rows, check, lib
 
 _TYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16, torch.float32: _lib.FP32}
 _LAYOUTS = {"half": 0, "pairs": 1}
@@ -35,6 +34,9 @@ def _on(t, name, device=None):
 
 
 def _ints(t, name, shape, device):
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == shape
+            and t.is_cuda and t.device == device and t.is_contiguous()):
+        return
     _on(t, name, device)
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
@@ -42,6 +44,24 @@ def _ints(t, name, shape, device):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, dev, *args):
+    """One C-ABI call on the current stream of device ``dev`` (its last
+    argument), with that device current, inside an NVTX range of its name."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(name, dev, *args)
+    push, pop = torch.cuda.nvtx.range_push, torch.cuda.nvtx.range_pop
+    push(name)
+    try:
+        check(getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
+    finally:
+        pop()
 
 
 def _rows(t, name, written=False):
@@ -165,10 +185,9 @@ def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=No
         qr, qo = (_rows(q, "q"), _rows(outs[0], "q_out", True)) if hq else (_NONE, _NONE)
         hkv = 0 if k is None else k.shape[1]
         kr, ko = (_rows(k, "k"), _rows(outs[1], "k_out", True)) if hkv else (_NONE, _NONE)
-        with torch.cuda.device(dev):
-            _call("pbs_rope", qr, qo, hq, kr, ko, hkv, _ptr(pos), 0 if pos.dim() == 1 else n,
-                  _ptr(inv_freq), gain, b, n, d, rot, _LAYOUTS[layout], int(bool(transpose)),
-                  _TYPES[q.dtype], _stream(dev))
+        _call("pbs_rope", dev, qr, qo, hq, kr, ko, hkv, _ptr(pos), 0 if pos.dim() == 1 else n,
+              _ptr(inv_freq), gain, b, n, d, rot, _LAYOUTS[layout], int(bool(transpose)),
+              _TYPES[q.dtype])
     return outs[0] if k is None else tuple(outs)
 
 
@@ -224,9 +243,8 @@ def cache_reserve(table, refs, lens, want, page):
     _ints(want, "want", (c.seqs,), dev)
     src, dst = (torch.empty(c.seqs, dtype=torch.int32, device=dev) for _ in range(2))
     ws, need = _ws(_lib.CACHE_RESERVE, c, 0, dev)
-    with torch.cuda.device(dev):
-        _call("pbs_cache_reserve", _ptr(table), _ptr(refs), _ptr(lens), _ptr(want), _ptr(src),
-              _ptr(dst), c, _ptr(ws), need, _stream(dev))
+    _call("pbs_cache_reserve", dev, _ptr(table), _ptr(refs), _ptr(lens), _ptr(want), _ptr(src),
+          _ptr(dst), c, _ptr(ws), need)
     return src, dst
 
 
@@ -248,9 +266,8 @@ def cache_append(k, v, k_pages, v_pages, table, start, count=None):
         _ints(count, "count", (c.seqs,), dev)
     if k.numel() == 0:
         return
-    with torch.cuda.device(dev):
-        _call("pbs_cache_append", _rows(k, "k"), _rows(v, "v"), k.shape[-2], _ptr(k_pages),
-              _ptr(v_pages), _ptr(table), _ptr(start), _ptr(count), c, _stream(dev))
+    _call("pbs_cache_append", dev, _rows(k, "k"), _rows(v, "v"), k.shape[-2], _ptr(k_pages),
+          _ptr(v_pages), _ptr(table), _ptr(start), _ptr(count), c)
 
 
 def cache_copy(k_pages, v_pages, src, dst):
@@ -264,9 +281,8 @@ def cache_copy(k_pages, v_pages, src, dst):
     _ints(dst, "dst", (src.numel(),), dev)
     n = src.numel()
     ws, need = _ws(_lib.CACHE_COPY, c, n, dev)
-    with torch.cuda.device(dev):
-        _call("pbs_cache_copy", _ptr(k_pages), _ptr(v_pages), _ptr(src), _ptr(dst), n, c, _ptr(ws),
-              need, _stream(dev))
+    _call("pbs_cache_copy", dev, _ptr(k_pages), _ptr(v_pages), _ptr(src), _ptr(dst), n, c,
+          _ptr(ws), need)
 
 
 def cache_fork(table, refs, lens, src, dst, page):
@@ -276,9 +292,8 @@ def cache_fork(table, refs, lens, src, dst, page):
     dev = table.device
     _ints(src, "src", (src.numel(),), dev)
     _ints(dst, "dst", (src.numel(),), dev)
-    with torch.cuda.device(dev):
-        _call("pbs_cache_fork", _ptr(table), _ptr(refs), _ptr(lens), _ptr(src), _ptr(dst),
-              src.numel(), c, _stream(dev))
+    _call("pbs_cache_fork", dev, _ptr(table), _ptr(refs), _ptr(lens), _ptr(src), _ptr(dst),
+          src.numel(), c)
 
 
 def cache_trim(table, refs, lens, keep, page):
@@ -287,8 +302,7 @@ def cache_trim(table, refs, lens, keep, page):
     c = _books(table, refs, lens, page)
     dev = table.device
     _ints(keep, "keep", (c.seqs,), dev)
-    with torch.cuda.device(dev):
-        _call("pbs_cache_trim", _ptr(table), _ptr(refs), _ptr(lens), _ptr(keep), c, _stream(dev))
+    _call("pbs_cache_trim", dev, _ptr(table), _ptr(refs), _ptr(lens), _ptr(keep), c)
 
 
 def cache_compact(k_pages, v_pages, table, refs):
@@ -299,9 +313,8 @@ def cache_compact(k_pages, v_pages, table, refs):
     _ints(refs, "refs", (c.pages,), dev)
     src, dst = torch.empty_like(refs), torch.empty_like(refs)
     ws, need = _ws(_lib.CACHE_COMPACT, c, 0, dev)
-    with torch.cuda.device(dev):
-        _call("pbs_cache_compact", _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(refs), _ptr(src),
-              _ptr(dst), c, _ptr(ws), need, _stream(dev))
+    _call("pbs_cache_compact", dev, _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(refs),
+          _ptr(src), _ptr(dst), c, _ptr(ws), need)
     return src, dst
 
 
@@ -319,9 +332,8 @@ def cache_accept(k_pages, v_pages, table, start, path, count=None, lens=None):
     for t, nm in ((count, "count"), (lens, "lens")):
         if t is not None:
             _ints(t, nm, (c.seqs,), dev)
-    with torch.cuda.device(dev):
-        _call("pbs_cache_accept", _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(start),
-              _ptr(path), _ptr(count), _ptr(lens), path.shape[1], c, _stream(dev))
+    _call("pbs_cache_accept", dev, _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(start),
+          _ptr(path), _ptr(count), _ptr(lens), path.shape[1], c)
 
 
 # ------------------------------------------------------------------ attention
@@ -338,9 +350,7 @@ def tree_mask(parents):
     b, t = parents.shape
     mask = torch.empty(b, t, (t + 31) // 32, dtype=torch.int32, device=parents.device)
     depth = torch.empty_like(parents)
-    with torch.cuda.device(parents.device):
-        _call("pbs_tree_mask", _ptr(parents), _ptr(mask), _ptr(depth), b, t,
-              _stream(parents.device))
+    _call("pbs_tree_mask", parents.device, _ptr(parents), _ptr(mask), _ptr(depth), b, t)
     return mask, depth
 
 
@@ -371,24 +381,28 @@ def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.
         _ints(count, "count", (c.seqs,), dev)
     if mask is not None:
         _ints(mask, "mask", (c.seqs, tree, (tree + 31) // 32), dev)
-    make = torch.empty if count is None else torch.zeros
+    zero = count is not None and out is None
     if out is None:
-        out = make(q.shape, dtype=q.dtype, device=dev)
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     else:
         _on(out, "out", dev)
         if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape and type")
         if out.data_ptr() == q.data_ptr() and out.numel():
             raise ValueError("out must not be q")
-    l = make(q.shape[:3], dtype=torch.float32, device=dev) if lse else None
+    if not lse:
+        l = None
+    elif zero or count is None:
+        l = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+    else:
+        l = torch.zeros(q.shape[:3], dtype=torch.float32, device=dev)
     need = lib().pbs_tree_workspace_bytes(hq, tree, c) if q.numel() else 0
     if ws is None or ws.numel() * ws.element_size() < need:
         ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     rows = _rows(q, "q") if q.numel() else _NONE
-    with torch.cuda.device(dev):
-        _call("pbs_tree_attn", rows, _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(start),
-              _ptr(count), _ptr(mask), _ptr(out), _ptr(l), hq, tree, c, scale, _TYPES[q.dtype],
-              _ptr(ws), need, _stream(dev))
+    _call("pbs_tree_attn", dev, rows, _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(start),
+          _ptr(count), _ptr(mask), _ptr(out), _ptr(l), hq, tree, c, scale, int(zero),
+          _TYPES[q.dtype], _ptr(ws), need)
     return (out, l) if lse else out
 
 

@@ -137,8 +137,8 @@ def test_empty_calls_launch_nothing():
     assert lib.pbs_cache_trim(*[None] * 4, none, None) == 0
     assert lib.pbs_cache_accept(*[None] * 7, 0, c, None) == 0
     assert lib.pbs_tree_mask(None, None, None, 0, 5, None) == 0
-    assert lib.pbs_tree_attn(r, *[None] * 8, 4, 0, c, 0.0, 0, None, 0, None) == 0
-    assert lib.pbs_tree_attn(r, *[None] * 8, 4, 3, none, 0.0, 0, None, 0, None) == 0
+    assert lib.pbs_tree_attn(r, *[None] * 8, 4, 0, c, 0.0, 0, 0, None, 0, None) == 0
+    assert lib.pbs_tree_attn(r, *[None] * 8, 4, 3, none, 0.0, 0, 0, None, 0, None) == 0
 
 
 @pytest.mark.parametrize("kw", [dict(layers=0), dict(pages=0), dict(hkv=0), dict(page=0),
@@ -191,7 +191,7 @@ def test_cache_pointers_and_workspaces():
 
 
 def call_tree(c, hq=4, tree=3, q=None, ptrs=None, dtype=0, ws=FAKE, ws_bytes=1 << 40):
-    return pbs.lib().pbs_tree_attn(q or rows(), *(ptrs or [FAKE] * 8), hq, tree, c, 0.0, dtype, ws,
+    return pbs.lib().pbs_tree_attn(q or rows(), *(ptrs or [FAKE] * 8), hq, tree, c, 0.0, 0, dtype, ws,
                                    ws_bytes, None)
 
 
@@ -199,7 +199,7 @@ def test_tree_refusals():
     bad, no = _lib.ERR_INVALID_ARG, _lib.ERR_UNSUPPORTED
     for kw in (dict(hkv=0), dict(seqs=-1), dict(pages=0), dict(width=0), dict(page=0)):
         assert call_tree(cache(**kw)) == bad
-    for kw in (dict(d=96), dict(page=8), dict(page=48), dict(page=512), dict(seqs=2049),
+    for kw in (dict(d=96), dict(page=8), dict(page=48), dict(page=512), dict(seqs=65536),
                dict(pages=1 << 27), dict(width=1 << 27)):
         assert call_tree(cache(**kw)) == no
         assert pbs.lib().pbs_tree_workspace_bytes(4, 3, cache(**kw)) == 0

@@ -449,10 +449,13 @@ class Tree:
         """Against the oracle. Logits: a sum of d products in fp32 (the tensor
         cores' sums may truncate: 2^-23 a step) of size at most |q||k|, then
         exponentials within 2^-21; P in two 16-bit parts is off by 2^-16 (bf16)
-        of itself; the n weights times V are added in fp32. The result rounds
-        by half a step, plus the smallest step in fp16."""
+        of itself, and in one part (items of more than 128 rows) by half a step
+        of itself, so their sum with V by half a step of the spread; the n
+        weights times V are added in fp32. The result rounds by half a step,
+        plus the smallest step in fp16."""
         hkv, g = self.k.shape[1], q.shape[1] // self.k.shape[1]
         d = q.shape[-1]
+        one_part = half_step(dtype) if g * q.shape[2] > 128 else 0.0
         for s, n in enumerate(self.len):
             for h in range(hkv):
                 k, v = (f64(x[h]) for x in self.rows[s])
@@ -462,7 +465,7 @@ class Tree:
                     want, wl, spread = dec.attend(qq, k, v, self.start[s], see[s][:c, :c], sigma)
                     size = sigma * (np.abs(qq) @ np.abs(np.nan_to_num(k)).T).max(initial=0.0)
                     logit = size * d * 2.0 ** -23 + 2.0 ** -21
-                    rel = 2 * logit + 2.0 ** -15 + n * 2.0 ** -23
+                    rel = 2 * logit + 2.0 ** -15 + n * 2.0 ** -23 + one_part
                     got, gl = f64(o[s, hq, :c]), f64(lse[s, hq, :c])
                     if (s, h) in wild:
                         ok = ~np.isfinite(want)
@@ -594,6 +597,46 @@ def test_long_context_split_over_every_sm(dev):
     # the parts are summed tile by tile, 64 keys at a time: n / 64 + 64 steps
     assert ((o[0, :, 0].double() - want).abs() <= half_step(BF16) * want.abs() + rel * spread).all()
     assert ((lse[0, :, 0].double() - torch.logsumexp(a, -1)).abs() <= rel).all()
+
+
+@pytest.mark.parametrize("tree,hq,hkv,b,most", [(64, 32, 8, 24, 900), (1, 32, 8, 150, 400),
+                                                (20, 16, 8, 40, 3000), (100, 8, 2, 9, 2000)])
+def test_many_items_in_a_run(tree, hq, hkv, b, most, dev):
+    """Batches whose CTAs work through several items each, drafts that span key
+    tiles in one after the other: against the formula in fp64 on the GPU, within
+    a step of the result plus a step of the spread."""
+    d, page, g = 128, 64, torch.Generator(dev).manual_seed(tree)
+    r = random.Random(b)
+    start = [r.randint(0, most) for _ in range(b)]
+    count = [r.randint(0, tree) if tree > 1 else 1 for _ in range(b)]
+    need = [-(-(s + c) // page) for s, c in zip(start, count)]
+    pages, width = sum(need) + 1, max(need)
+    perm = torch.randperm(pages, generator=torch.Generator().manual_seed(b)).tolist()
+    table = torch.full((b, width), -1, dtype=torch.int32)
+    for s in range(b):
+        for j in range(need[s]):
+            table[s, j] = perm.pop()
+    k, v = (torch.randn(pages, hkv, page, d, generator=g, device=dev).to(BF16) for _ in range(2))
+    q = (2 * torch.randn(b, hq, tree, d, generator=g, device=dev)).to(BF16)
+    parents = [[-1 if i == 0 else r.randrange(max(0, i - 5), i) for i in range(tree)]] * b
+    mask = pbs.tree_mask(i32(parents, dev))[0]
+    o, lse = pbs.tree_attn(q, k, v, table.to(dev), i32(start, dev), mask, i32(count, dev), lse=True)
+    assert pbs.device_status() == 0
+    see = torch.from_numpy(dec.visible(parents[0], tree)).to(dev)
+    for s in range(b):
+        c, n = count[s], start[s] + count[s]
+        assert not o[s, :, c:].any() and not lse[s, :, c:].any()
+        if not c:
+            continue
+        at = table[s, :need[s]].to(dev).long()
+        kk, vv = (x[at].transpose(0, 1).reshape(hkv, -1, d)[:, :n].double().repeat_interleave(
+            hq // hkv, 0) for x in (k, v))
+        a = q[s, :, :c].double() @ kk.transpose(1, 2) / math.sqrt(d)
+        a[:, :, start[s]:] = a[:, :, start[s]:].masked_fill(~see[:c, :c], -math.inf)
+        p = torch.softmax(a, -1)
+        tol = half_step(BF16) * (p @ vv).abs() + 2 * half_step(BF16) * (p @ vv.abs())
+        assert ((o[s, :, :c].double() - p @ vv).abs() <= tol).all()
+        assert (lse[s, :, :c].double() - torch.logsumexp(a, -1)).abs().max() < 1e-3
 
 
 def test_tree_attn_refuses(dev):
