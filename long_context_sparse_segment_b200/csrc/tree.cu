@@ -8,7 +8,7 @@
 // once per item and serves them all. With few rows this is bound by reading
 // the cache.
 //
-// This kernel: up to 32 rows an item, warp MMA. Eight warps take tiles of 64
+// This kernel: up to 16 rows an item, warp MMA. Eight warps take tiles of 64
 // keys, four warps a tile (16 keys each) and the two halves in turn, each
 // with its own maximum, sum and output, joined when the item ends; a ninth
 // warp brings the tiles by TMA, page by page, into a ring.
@@ -25,10 +25,10 @@ constexpr int kKeys = 64;       // keys of a unit
 constexpr int kConsumers = 8;   // warps
 constexpr int kMmaThreads = 32 * (kConsumers + 1);
 
-template <int D, int MT>
+template <int D>
 struct MmaCfg {
   static constexpr int H = D / 64;
-  static constexpr int ROWS = 16 * MT;
+  static constexpr int ROWS = 16;
   static constexpr uint32_t KV = kKeys * D * 2;   // bytes of a K or V tile
   static constexpr int ST = D == 128 ? 4 : 8;     // even: a stage stays with one half
   static constexpr int PAD = 4;                   // floats behind a joined row
@@ -41,13 +41,13 @@ struct MmaCfg {
   };
   static constexpr size_t SMEM = 1024 + 2 * KV * ST + ROWS * D * 2 + JOIN + sizeof(Bars);
 };
-static_assert(MmaCfg<128, 2>::SMEM <= 232448 && MmaCfg<64, 2>::SMEM <= 232448, "shared memory");
+static_assert(MmaCfg<128>::SMEM <= 232448 && MmaCfg<64>::SMEM <= 232448, "shared memory");
 
-template <typename T, int D, int MT>
+template <typename T, int D>
 __global__ void __launch_bounds__(kMmaThreads, 1)
     tree_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a) {
-  using C = MmaCfg<D, MT>;
+  using C = MmaCfg<D>;
   constexpr int H = C::H, ST = C::ST, ROWS = C::ROWS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>(
@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     bar->abort = 0, bar->bad = 0;
     fence_barrier_init();
   }
+  allow_next();
   if (!find_place<ROWS, kKeys, kMmaThreads>(a, &bar->place)) return;
   Walk<ROWS, kKeys> walk(bar->place);
   Segment g;
@@ -143,23 +144,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     if (tid == 0) bar->bad = 0;
     if (!sync()) return;
-    // drafts of this thread's rows
-    int draft[MT][2];
+    int draft[2];  // of this thread's rows
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int x = 0; x < 2; ++x) draft[x] = min((g.rt * ROWS + gr + 8 * x) / a.G, g.count - 1);
+    uint32_t q[D / 16][4];
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        draft[mt][x] = min((g.rt * ROWS + mt * 16 + gr + 8 * x) / a.G, g.count - 1);
-    float m[MT][2], l[MT][2], o[MT][D / 8][4];
+    for (int kk = 0; kk < D / 16; ++kk)
+      ldsm_x4(q[kk], sQ + swz<D>(lane & 15, kk * 16 + ((lane >> 4) << 3)));
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) m[mt][x] = -INFINITY, l[mt][x] = 0.f;
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     bool bad = false;
     for (int k = g.k0; k < g.k1; ++k, ++it) {
       if ((it & 1) != half_id) continue;
@@ -169,13 +165,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       const int key0 = k * kKeys + key16;  // this warp's 16 keys
       if (key0 < len) {
         // S = Q K^T
-        float s[MT][2][4];
+        float s[2][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
         {
           const int row = key16 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
@@ -183,68 +177,57 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const int ch = kk * 2 + ((lane >> 3) & 1);
             uint32_t b[4];
             ldsm_x4(b, tK + (ch >> 3) * (kKeys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              uint32_t q[4];
-              ldsm_x4(q, sQ + swz<D>(mt * 16 + (lane & 15), kk * 16 + ((lane >> 4) << 3)));
-              Two<T>::mma(s[mt][0], q, b[0], b[1]);
-              Two<T>::mma(s[mt][1], q, b[2], b[3]);
-            }
+            Two<T>::mma(s[0], q[kk], b[0], b[1]);
+            Two<T>::mma(s[1], q[kk], b[2], b[3]);
           }
         }
         // masks: drafts, and keys behind the last token
-        if (key0 + 16 > g.start) {
+        const bool edge = key0 + 16 > g.start;
+        if (edge) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t seen = seen_word(a, g, draft[x], key0) >> qc;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t seen = seen_word(a, g, draft[mt][x], key0) >> qc;
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (!(seen >> (n * 8 + e) & 1)) s[mt][n][2 * x + e] = -INFINITY;
-            }
+              for (int e = 0; e < 2; ++e)
+                if (!(seen >> (n * 8 + e) & 1)) s[n][2 * x + e] = -INFINITY;
+          }
         }
         // running maximum, P in two 16-bit parts: 16 bits alone would add as
         // much error as the output's own rounding
-        uint32_t hi[MT][4], lo[MT][4];
+        uint32_t hi[4], lo[4];
+        float alpha[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          float alpha[2];
+        for (int x = 0; x < 2; ++x) {
+          float t = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+          const float top = fmaxf(m[x], t * a.sl2);
+          alpha[x] = part_scale(m[x], top);
+          m[x] = top;
+          const float mu = top == -INFINITY ? 0.f : top;
+          float sum = 0.f;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float t = fmaxf(fmaxf(s[mt][0][2 * x], s[mt][0][2 * x + 1]),
-                            fmaxf(s[mt][1][2 * x], s[mt][1][2 * x + 1]));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-            const float top = fmaxf(m[mt][x], t * a.sl2);
-            alpha[x] = m[mt][x] == top ? 1.f : ex2_approx(m[mt][x] - top);
-            m[mt][x] = top;
-            const float mu = top == -INFINITY ? 0.f : top;
-            float sum = 0.f;
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const float p0 = ex2_approx(fmaf(s[mt][n][2 * x], a.sl2, -mu));
-              const float p1 = ex2_approx(fmaf(s[mt][n][2 * x + 1], a.sl2, -mu));
-              sum += p0 + p1;
-              const uint32_t h = Two<T>::pack(p0, p1);
-              const float2 f = Two<T>::unpack(h);
-              hi[mt][2 * n + x] = h;
-              lo[mt][2 * n + x] = Two<T>::pack(p0 - f.x, p1 - f.y);
-            }
-            l[mt][x] = l[mt][x] * alpha[x] + sum;
+          for (int n = 0; n < 2; ++n) {
+            const float p0 = ex2_approx(fmaf(s[n][2 * x], a.sl2, -mu));
+            const float p1 = ex2_approx(fmaf(s[n][2 * x + 1], a.sl2, -mu));
+            sum += p0 + p1;
+            const uint32_t w = Two<T>::pack(p0, p1);
+            const float2 f = Two<T>::unpack(w);
+            hi[2 * n + x] = w;
+            lo[2 * n + x] = Two<T>::pack(p0 - f.x, p1 - f.y);
           }
-          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+          l[x] = l[x] * alpha[x] + sum;
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
+          for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[mt][n][e] *= alpha[e >> 1];
-          }
+            for (int e = 0; e < 4; ++e) o[n][e] *= alpha[e >> 1];
         }
         // O += P V; V rows behind the last token are left out, and NaN or
         // infinity in a drafted row (see add_wild)
-        const bool edge = key0 + 16 > g.start;
         unsigned keep[2] = {3, 3}, drafted[2] = {0, 0};
         if (edge) {
 #pragma unroll
@@ -264,13 +247,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
             for (int x = 0; x < 4; ++x) b[x] = clean2<T>(b[x], keep[x & 1], drafted[x & 1], &bad);
           }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            Two<T>::mma(o[mt][2 * n], hi[mt], b[0], b[1]);
-            Two<T>::mma(o[mt][2 * n + 1], hi[mt], b[2], b[3]);
-            Two<T>::mma(o[mt][2 * n], lo[mt], b[0], b[1]);
-            Two<T>::mma(o[mt][2 * n + 1], lo[mt], b[2], b[3]);
-          }
+          Two<T>::mma(o[2 * n], hi, b[0], b[1]);
+          Two<T>::mma(o[2 * n + 1], hi, b[2], b[3]);
+          Two<T>::mma(o[2 * n], lo, b[0], b[1]);
+          Two<T>::mma(o[2 * n + 1], lo, b[2], b[3]);
         }
       }
       warp_arrive(&bar->empty[st], lane);
@@ -278,70 +258,62 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     // ------------------------------------------------ join the eight warps
     if (__any_sync(0xffffffffu, bad) && lane == 0) bar->bad = 1;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float t = l[mt][x];
-        t += __shfl_xor_sync(0xffffffffu, t, 1);
-        t += __shfl_xor_sync(0xffffffffu, t, 2);
-        if ((lane & 3) == 0) bar->ml[warp][mt * 16 + gr + 8 * x] = make_float2(m[mt][x], t);
-      }
-    const int slot = 2 * blockIdx.x + (seg > 0);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt * 16 < rows) {
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (mt * 16 + gr + 8 * x < rows)
-              *reinterpret_cast<float2 *>(join + (warp * 16 + gr + 8 * x) * (D + C::PAD) + n * 8 +
-                                          qc) = make_float2(o[mt][n][2 * x], o[mt][n][2 * x + 1]);
-      }
-      if (!sync()) return;
-      constexpr int N = D / 16;  // columns a thread joins: 16 threads a row
-      const int r = mt * 16 + (tid >> 4), col = (tid & 15) * N;
-      if (r < rows) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, bar->ml[w][r].x);
-        float sum = 0.f, acc[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kConsumers; ++w) {
-          const float2 ml = bar->ml[w][r];
-          const float f = part_scale(ml.x, top);
-          const float *src = join + (w * 16 + (r & 15)) * (D + C::PAD) + col;
-          sum += ml.y * f;
-#pragma unroll
-          for (int e = 0; e < N; e += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(src + e);
-            acc[e] += v.x * f, acc[e + 1] += v.y * f;
-            acc[e + 2] += v.z * f, acc[e + 3] += v.w * f;
-          }
-        }
-        const int rr = g.rt * ROWS + r;
-        if (g.whole) {
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-          for (int e = 0; e < N; ++e) acc[e] *= inv;
-          if (*(volatile int *)&bar->bad)
-            add_wild<T, N>(a, g.s, g.h, Seq{g.start, g.count}, rr / a.G, D, col, acc);
-          write_row<T, N>(a, g.s, g.h, rr, D, col, acc);
-          if (col == 0) write_lse(a, g.s, g.h, rr, top, sum);
-        } else {
-          float *dst = a.part_o + ((size_t)slot * ROWS + r) * D + col;
-#pragma unroll
-          for (int e = 0; e < N; e += 4)
-            *reinterpret_cast<float4 *>(dst + e) =
-                make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-          if (col == 0) a.part_ml[(size_t)slot * ROWS + r] = make_float2(top, sum);
-          if (tid == 0 && mt == 0) a.part_bad[slot] = bar->bad;
-        }
-      }
-      if (!sync()) return;  // the join buffer and Q are free again
+    for (int x = 0; x < 2; ++x) {
+      float t = l[x];
+      t += __shfl_xor_sync(0xffffffffu, t, 1);
+      t += __shfl_xor_sync(0xffffffffu, t, 2);
+      if ((lane & 3) == 0) bar->ml[warp][gr + 8 * x] = make_float2(m[x], t);
     }
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (gr + 8 * x < rows)
+          *reinterpret_cast<float2 *>(join + (warp * 16 + gr + 8 * x) * (D + C::PAD) + n * 8 + qc) =
+              make_float2(o[n][2 * x], o[n][2 * x + 1]);
+    if (!sync()) return;
+    const int slot = 2 * blockIdx.x + (seg > 0);
+    constexpr int N = D / 16;  // columns a thread joins: 16 threads a row
+    const int r = tid & 15, col = (tid >> 4) * N;
+    if (r < rows) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, bar->ml[w][r].x);
+      float sum = 0.f, acc[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) {
+        const float2 ml = bar->ml[w][r];
+        const float f = part_scale(ml.x, top);
+        const float *src = join + (w * 16 + r) * (D + C::PAD) + col;
+        sum += ml.y * f;
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(src + e);
+          acc[e] += v.x * f, acc[e + 1] += v.y * f;
+          acc[e + 2] += v.z * f, acc[e + 3] += v.w * f;
+        }
+      }
+      const int rr = g.rt * ROWS + r;
+      if (g.whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] *= inv;
+        if (*(volatile int *)&bar->bad)
+          add_wild<T, N>(a, g.s, g.h, Seq{g.start, g.count}, rr / a.G, D, col, acc);
+        write_row<T, N>(a, g.s, g.h, rr, D, col, acc);
+        if (col == 0) write_lse(a, g.s, g.h, rr, top, sum);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; e += 4)
+          a.part_o[((size_t)slot * (D / 4) + (col + e) / 4) * ROWS + r] =
+              make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+        if (col == 0) a.part_ml[(size_t)slot * ROWS + r] = make_float2(top, sum);
+        if (tid == 0) a.part_bad[slot] = *(volatile int *)&bar->bad;
+      }
+    }
+    if (!sync()) return;  // the join buffer and Q are free again
   }
 }
 
@@ -421,11 +393,11 @@ Parts parts(int rows, int d) {
   return p;
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D>
 cudaError_t run_mma(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int grid,
                     cudaStream_t st) {
-  using C = MmaCfg<D, MT>;
-  constexpr auto kern = tree_mma_kernel<T, D, MT>;
+  using C = MmaCfg<D>;
+  constexpr auto kern = tree_mma_kernel<T, D>;
   const cudaError_t e = allow_smem<kern>((int)C::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<grid, kMmaThreads, C::SMEM, st>>>(mk, mv, a);
@@ -478,7 +450,7 @@ pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
   TreeArgs a{};
   a.q = q, a.table = table, a.start = start, a.count = count, a.mask = mask, a.v_pages = v_pages;
   a.out = out, a.lse = lse;
-  a.part_o = (float *)((uint8_t *)ws + p.o);
+  a.part_o = (float4 *)((uint8_t *)ws + p.o);
   a.part_ml = (float2 *)((uint8_t *)ws + p.ml);
   a.part_bad = (int *)((uint8_t *)ws + p.bad);
   a.err = error_word();
@@ -499,11 +471,11 @@ pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
   if (rows > 16)
     e = launch_tree_tc(mk, mv, a, c.d, rows, bf16, grid, cs);
   else if (c.d == 64)
-    e = bf16 ? run_mma<__nv_bfloat16, 64, 1>(mk, mv, a, grid, cs)
-             : run_mma<__half, 64, 1>(mk, mv, a, grid, cs);
+    e = bf16 ? run_mma<__nv_bfloat16, 64>(mk, mv, a, grid, cs)
+             : run_mma<__half, 64>(mk, mv, a, grid, cs);
   else
-    e = bf16 ? run_mma<__nv_bfloat16, 128, 1>(mk, mv, a, grid, cs)
-             : run_mma<__half, 128, 1>(mk, mv, a, grid, cs);
+    e = bf16 ? run_mma<__nv_bfloat16, 128>(mk, mv, a, grid, cs)
+             : run_mma<__half, 128>(mk, mv, a, grid, cs);
   return e == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
 }
 

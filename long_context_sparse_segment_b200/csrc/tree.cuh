@@ -32,7 +32,7 @@ struct TreeArgs {
   const void *v_pages;  // for the non-finite rows of drafts
   void *out;
   float *lse;
-  float *part_o;    // [2 grid][rows][d]
+  float4 *part_o;   // [2 grid][d / 4][rows]: neighbouring rows side by side
   float2 *part_ml;  // [2 grid][rows]: running maximum (log2) and sum
   int *part_bad;    // [2 grid]: drafted V rows with NaN or infinity met
   int *err;
@@ -87,19 +87,25 @@ struct Place {
 };
 
 // Every thread of the block (NT of them, a multiple of 32) calls it; false
-// for a CTA without units.
+// for a CTA without units. Ends with a barrier where it returns true.
 template <int ROWS, int KEYS, int NT>
 __device__ __forceinline__ bool find_place(const TreeArgs &a, Place *p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto units = [&](int s) { return s < a.seqs ? units_of<ROWS, KEYS>(a, seq_of(a, s)) : 0; };
-  int sum = 0;
-  for (int s = tid; s < a.seqs; s += NT) sum += units(s);
+  // up to 32 sequences every warp holds them all; more are summed by the block
+  // first (one more barrier and a second look at the lengths: 0.7 us more)
+  int x = units(a.seqs <= 32 ? lane : tid), sum = x, total = 0;
+  if (a.seqs > 32)
+    for (int s = tid + NT; s < a.seqs; s += NT) sum += units(s);
   sum = __reduce_add_sync(0xffffffffu, sum);
-  if (lane == 0) p->sum[warp] = sum;
-  __syncthreads();
-  int total = 0;
+  if (a.seqs <= 32) {
+    total = sum;
+  } else {
+    if (lane == 0) p->sum[warp] = sum;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) total += p->sum[w];
+    for (int w = 0; w < NT / 32; ++w) total += p->sum[w];
+  }
   const int runs = min(total, (int)gridDim.x);
   if ((int)blockIdx.x >= runs) return false;
   const Runs run(total, runs);
@@ -107,7 +113,7 @@ __device__ __forceinline__ bool find_place(const TreeArgs &a, Place *p) {
   if (warp == 0) {
     int base = 0;
     for (int s0 = 0;; s0 += 32) {
-      const int x = units(s0 + lane);
+      if (s0 > 0) x = units(s0 + lane);
       int inc = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -287,26 +293,57 @@ __device__ __forceinline__ float part_scale(float m, float top) {
 }
 
 // -------------------------------------------------------------------- combine
-// One warp per row of an item that several CTAs worked on: their parts, in
-// order, scaled to the common maximum. Bound by latency: a part is read once.
-constexpr int kCombineThreads = 128;
+// Joins the parts of the rows that several CTAs worked on. A block takes RB
+// rows of one (sequence, KV head): a thread holds 4 columns of a row and every
+// PG-th part of it, in order; the PG partial results are joined in shared
+// memory. It is launched while the attention kernel still runs (programmatic
+// dependent launch): what comes before the wait reads only the call's inputs.
+// Bound by latency: a part is read once, all of a thread's reads in flight.
+constexpr int kCombineThreads = 512;
 
-template <typename T, int D, int ROWS, int KEYS>
+// Allows the kernel launched behind this one to start.
+__device__ __forceinline__ void allow_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Waits until the kernel launched before this one has ended, its writes visible.
+__device__ __forceinline__ void wait_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+struct Part {
+  float m, l;
+  float4 o;
+};
+
+__device__ __forceinline__ void join(Part &p, const Part &q) {
+  const float top = fmaxf(p.m, q.m), f = part_scale(p.m, top), g = part_scale(q.m, top);
+  p.m = top, p.l = p.l * f + q.l * g;
+  p.o.x = p.o.x * f + q.o.x * g, p.o.y = p.o.y * f + q.o.y * g;
+  p.o.z = p.o.z * f + q.o.z * g, p.o.w = p.o.w * f + q.o.w * g;
+}
+
+template <typename T, int D, int ROWS, int KEYS, int RB>
 __global__ void __launch_bounds__(kCombineThreads)
     tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
-  __shared__ int sh[8];
+  constexpr int C4 = D / 4, PG = kCombineThreads / (RB * C4);
+  static_assert(PG * RB * C4 == kCombineThreads, "threads");
+  __shared__ int sh[2 * kCombineThreads / 32];
+  __shared__ float4 so[kCombineThreads];
+  __shared__ float2 sml[PG][RB];
   const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r0 = blockIdx.x * RB;  // first row of the (sequence, KV head)
   const Seq q = seq_of(a, s);
-  if (a.zero_rest) {
-    const int r = blockIdx.x * 4 + warp;
-    if (r >= q.count * a.G && r < a.tree * a.G) {
-      constexpr int N = D / 32;
-      const float o[N] = {};
-      write_row<T, N>(a, s, h, r, D, lane * N, o);
-      if (lane == 0 && a.lse) a.lse[((size_t)s * a.hq + h * a.G + r % a.G) * a.tree + r / a.G] = 0.f;
-    }
+  const int rows = q.count * a.G;
+  // rows of the results: thread -> (row, 4 columns), neighbours along the row
+  const int wr = r0 + tid / C4, wc = tid % C4 * 4;
+  const bool writes = tid < RB * C4;
+  if (a.zero_rest && writes && wr >= rows && wr < a.tree * a.G) {
+    const float o[4] = {};
+    write_row<T, 4>(a, s, h, wr, D, wc, o);
+    if (wc == 0 && a.lse)
+      a.lse[((size_t)s * a.hq + h * a.G + wr % a.G) * a.tree + wr / a.G] = 0.f;
   }
-  if (blockIdx.x * 4 >= q.count * a.G) return;
+  if (r0 >= rows) return;
   // units before this sequence, and all
   int mine = 0, all = 0;
   for (int i = tid; i < a.seqs; i += kCombineThreads) {
@@ -316,60 +353,79 @@ __global__ void __launch_bounds__(kCombineThreads)
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
   all = __reduce_add_sync(0xffffffffu, all);
-  if (lane == 0) sh[warp] = mine, sh[4 + warp] = all;
+  constexpr int W = kCombineThreads / 32;
+  if (lane == 0) sh[warp] = mine, sh[W + warp] = all;
   __syncthreads();
-  const int r = blockIdx.x * 4 + warp;  // row of the (sequence, KV head)
-  if (r >= q.count * a.G) return;
-  const int total = sh[4] + sh[5] + sh[6] + sh[7], runs = min(total, grid);
-  const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(q.count * a.G, ROWS);
-  const int u0 = sh[0] + sh[1] + sh[2] + sh[3] + (h * rts + r / ROWS) * kt;
-  const Runs run(total, runs);
+  int u0 = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) u0 += sh[w], total += sh[W + w];
+  const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(rows, ROWS);
+  u0 += (h * rts + r0 / ROWS) * kt;
+  const Runs run(total, min(total, grid));
   const int c0 = run.owner(u0), c1 = run.owner(u0 + kt - 1);
   if (c0 == c1) return;
   const int slot0 = 2 * c0 + (run.start(c0) != u0);
-  auto slot = [&](int c) { return c == c0 ? slot0 : 2 * c; };
-  const int rr = r % ROWS;
-  float top = -INFINITY;
+  wait_previous();
+  const int r = tid % RB, c4 = tid / RB % C4, pg = tid / (RB * C4);
+  const bool live = r0 + r < rows;
+  Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   int bad = 0;
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    top = fmaxf(top, a.part_ml[(size_t)slot(c) * ROWS + rr].x);
-    bad |= a.part_bad[slot(c)];
-  }
-  top = warp_max(top);
-  bad = __any_sync(0xffffffffu, bad);
-  constexpr int N = D / 32;
-  const int col = lane * N;
-  float acc[N], sum = 0.f;
-#pragma unroll
-  for (int e = 0; e < N; ++e) acc[e] = 0.f;
+  if (live) {
+    const int rr = r0 % ROWS + r;
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const size_t at = (size_t)slot(c) * ROWS + rr;
-    const float2 ml = a.part_ml[at];
-    const float f = part_scale(ml.x, top);
-    sum += ml.y * f;
-    const float *src = a.part_o + at * D + col;
-    if constexpr (N == 4) {
-      const float4 v = *reinterpret_cast<const float4 *>(src);
-      acc[0] += v.x * f, acc[1] += v.y * f, acc[2] += v.z * f, acc[3] += v.w * f;
-    } else {
-      const float2 v = *reinterpret_cast<const float2 *>(src);
-      acc[0] += v.x * f, acc[1] += v.y * f;
+    for (int c = c0 + pg; c <= c1; c += PG) {
+      const size_t slot = c == c0 ? slot0 : 2 * c;
+      const float2 ml = a.part_ml[slot * ROWS + rr];
+      join(p, Part{ml.x, ml.y, a.part_o[(slot * C4 + c4) * ROWS + rr]});
+      bad |= a.part_bad[slot];
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (PG > 1) {
+    so[tid] = p.o;
+    if (c4 == 0) sml[pg][r] = make_float2(p.m, p.l);
+    bad = __syncthreads_or(bad);
+    if (pg == 0) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) acc[e] *= inv;
-  if (bad) add_wild<T, N>(a, s, h, q, r / a.G, D, col, acc);
-  write_row<T, N>(a, s, h, r, D, col, acc);
-  if (lane == 0) write_lse(a, s, h, r, top, sum);
+      for (int g = 1; g < PG; ++g)
+        join(p, Part{sml[g][r].x, sml[g][r].y, so[tid + g * RB * C4]});
+    }
+    __syncthreads();
+  } else {
+    bad = __syncthreads_or(bad);
+  }
+  if (pg == 0) {
+    so[r * C4 + c4] = p.o;
+    if (c4 == 0) sml[0][r] = make_float2(p.m, p.l);
+  }
+  __syncthreads();
+  if (!writes || wr >= rows) return;
+  const float2 ml = sml[0][tid / C4];
+  const float4 v = so[tid];
+  const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+  float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+  if (bad) add_wild<T, 4>(a, s, h, q, wr / a.G, D, wc, o);
+  write_row<T, 4>(a, s, h, wr, D, wc, o);
+  if (wc == 0) write_lse(a, s, h, wr, ml.x, ml.y);
 }
 
 template <typename T, int D, int ROWS, int KEYS>
 cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
-  const dim3 blocks((unsigned)ceil_div((int64_t)a.G * a.tree, 4), a.hkv, a.seqs);
-  tree_combine_kernel<T, D, ROWS, KEYS><<<blocks, kCombineThreads, 0, st>>>(a, grid);
-  return cudaGetLastError();
+  // 4 rows a block, and 16 where that makes more blocks than fit the GPU at
+  // once (four an SM)
+  const int64_t rows = (int64_t)a.G * a.tree, few = ceil_div(rows, 4) * a.hkv * a.seqs;
+  const int rb = few <= 4 * 148 ? 4 : 16;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ceil_div(rows, rb), a.hkv, a.seqs);
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return rb == 4
+             ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, KEYS, 4>, a, grid)
+             : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, KEYS, 16>, a, grid);
 }
 
 }  // namespace tree

@@ -88,6 +88,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto *sh = reinterpret_cast<typename C::Shared *>(sV + VS * C::TILE);
   volatile int *abort = &sh->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem, 512);
+    tmem_relinquish();
+  }
   if (tid == 0) {
     mbar_init(&sh->q_full, 8);
     mbar_init(&sh->seg, 8);
@@ -106,14 +110,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh->abort = 0;
     fence_barrier_init();
   }
-  // its barriers also publish the initialisation
-  if (!find_place<ROWS, kTile, kThreads>(a, &sh->place)) return;
-  if (warp == 1) {
-    tmem_alloc(&sh->tmem, 512);
-    tmem_relinquish();
-  }
+  allow_next();
   tc_fence_before();
-  __syncthreads();
+  // its last barrier publishes the initialisation
+  if (!find_place<ROWS, kTile, kThreads>(a, &sh->place)) {
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(sh->tmem, 512);
+    return;
+  }
   tc_fence_after();
   const uint32_t tbase = sh->tmem;
   Walk<ROWS, kTile> walk(sh->place);
@@ -350,16 +355,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Q: free once everybody is through with the segment before
     ok = seg_sync();
     if (!ok) break;
-    for (int e = tid - 128; e < ROWS * (D / 8); e += 256) {
-      const int r = e / (D / 8), ch = e % (D / 8);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const int rr = g.rt * ROWS + r, i = rr / a.G, hd = g.h * a.G + rr - i * a.G;
-        v = *reinterpret_cast<const uint4 *>((const T *)a.q.p + (int64_t)g.s * a.q.batch +
-                                             hd * a.q.head + i * a.q.row + ch * 8);
+    {
+      constexpr int CPR = D / 8, STEP = 256 / CPR, LOADS = ROWS / STEP,
+                    BATCH = LOADS < 8 ? LOADS : 8;
+      const int ch = (tid - 128) % CPR, rq = (tid - 128) / CPR;
+#pragma unroll 1
+      for (int e0 = 0; e0 < LOADS; e0 += BATCH) {
+        uint4 v[BATCH];
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+          const int r = rq + (e0 + e) * STEP;
+          v[e] = make_uint4(0, 0, 0, 0);
+          if (r < rows) {
+            const int rr = g.rt * ROWS + r, i = rr / a.G, hd = g.h * a.G + rr - i * a.G;
+            v[e] = *reinterpret_cast<const uint4 *>((const T *)a.q.p + (int64_t)g.s * a.q.batch +
+                                                    hd * a.q.head + i * a.q.row + ch * 8);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+          const int r = rq + (e0 + e) * STEP;
+          *reinterpret_cast<uint4 *>(sQ + (r / kTile) * C::TILE + (ch >> 3) * C::HALF +
+                                     (r % kTile) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[e];
+        }
       }
-      *reinterpret_cast<uint4 *>(sQ + (r / kTile) * C::TILE + (ch >> 3) * C::HALF +
-                                 (r % kTile) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
     }
     fence_proxy_async_smem();
     warp_arrive(&sh->q_full, lane);
@@ -516,11 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               write_row<T, 8>(a, g.s, g.h, rr, D, col + e, y);
             }
           } else {
-            float4 *dst =
-                reinterpret_cast<float4 *>(a.part_o + ((size_t)slot * ROWS + row) * D + col);
+            float4 *dst = a.part_o + ((size_t)slot * (D / 4) + col / 4) * ROWS + row;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              dst[e * ROWS] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
         __syncwarp();

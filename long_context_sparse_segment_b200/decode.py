@@ -22,6 +22,12 @@ _TYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16, torch.float32: _l
 _LAYOUTS = {"half": 0, "pairs": 1}
 _HALVES = (torch.bfloat16, torch.float16)
 _NONE = Rows(None, 0, 0, 0, 0)
+_VEC = {torch.bfloat16: 7, torch.float16: 7, torch.float32: 3}  # elements of 16 bytes, less one
+
+
+def _fresh(t):
+    """A new contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _on(t, name, device=None):
@@ -56,23 +62,26 @@ def _call(name, dev, *args):
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call(name, dev, *args)
-    push, pop = torch.cuda.nvtx.range_push, torch.cuda.nvtx.range_pop
-    push(name)
+    torch.cuda.nvtx.range_push(name)
     try:
         check(getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
     finally:
-        pop()
+        torch.cuda.nvtx.range_pop()
 
 
 def _rows(t, name, written=False):
     """[..., b, h, n, d] (4 or 5 dimensions) as pbs_rows: the head dimension
-    contiguous, the others multiples of 16 bytes."""
-    size, stride = t.shape, t.stride()
+    contiguous, the others multiples of 16 bytes; a tensor that is written may
+    not overlap itself."""
+    stride, p, odd = t.stride(), t.data_ptr(), _VEC[t.dtype]
+    if not written and len(stride) == 4 and stride[3] == 1 and not (
+            p & 15 or (stride[0] | stride[1] | stride[2]) & odd):
+        return Rows(p, 0, stride[0], stride[1], stride[2])
+    size = t.shape
     if size[-1] > 1 and stride[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     step = [st if n > 1 else 0 for n, st in zip(size[:-1], stride[:-1])]
-    vec = 16 // t.element_size()
-    if t.data_ptr() % 16 or any(x % vec for x in step):
+    if p & 15 or any(x & odd for x in step):
         raise ValueError(f"{name}: rows must be 16-byte aligned")
     if written:
         used = size[-1]
@@ -80,7 +89,7 @@ def _rows(t, name, written=False):
             if st < used:
                 raise ValueError(f"{name}: an output may not overlap itself")
             used = st * (n - 1) + used
-    return Rows(t.data_ptr(), step[0] if len(step) == 4 else 0, *step[-3:])
+    return Rows(p, step[0] if len(step) == 4 else 0, *step[-3:])
 
 
 def rope_freqs(rot, base=10000.0, scaling=None, device=None):
@@ -168,23 +177,24 @@ def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=No
     if rot % 16 or rot > d:
         raise ValueError("inv_freq: 2 * len must be a multiple of 16 and at most d")
     _ints(pos, "pos", (n,) if isinstance(pos, torch.Tensor) and pos.dim() == 1 else (b, n), dev)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
     outs = []
     for x, y, nm in ((q, q_out, "q_out"), (k, k_out, "k_out")):
         if x is None:
-            if y is not None:
-                raise ValueError("k_out without k")
             continue
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        else:
+        if y is not None:
             _on(y, nm, dev)
             if y.shape != x.shape or y.dtype != x.dtype:
                 raise ValueError(f"{nm} must have the shape and type of its input")
-        outs.append(y)
-    if b and n and q.numel() + (k.numel() if k is not None else 0):
-        qr, qo = (_rows(q, "q"), _rows(outs[0], "q_out", True)) if hq else (_NONE, _NONE)
-        hkv = 0 if k is None else k.shape[1]
-        kr, ko = (_rows(k, "k"), _rows(outs[1], "k_out", True)) if hkv else (_NONE, _NONE)
+        outs.append(_fresh(x) if y is None else y)
+    hkv = 0 if k is None else k.shape[1]
+    if b and n and hq + hkv:
+        qr = kr = qo = ko = _NONE
+        if hq:
+            qr, qo = _rows(q, "q"), _rows(outs[0], "q_out", q_out is not None)
+        if hkv:
+            kr, ko = _rows(k, "k"), _rows(outs[1], "k_out", k_out is not None)
         _call("pbs_rope", dev, qr, qo, hq, kr, ko, hkv, _ptr(pos), 0 if pos.dim() == 1 else n,
               _ptr(inv_freq), gain, b, n, d, rot, _LAYOUTS[layout], int(bool(transpose)),
               _TYPES[q.dtype])
@@ -241,7 +251,7 @@ def cache_reserve(table, refs, lens, want, page):
     c = _books(table, refs, lens, page)
     dev = table.device
     _ints(want, "want", (c.seqs,), dev)
-    src, dst = (torch.empty(c.seqs, dtype=torch.int32, device=dev) for _ in range(2))
+    src, dst = torch.empty_like(lens), torch.empty_like(lens)
     ws, need = _ws(_lib.CACHE_RESERVE, c, 0, dev)
     _call("pbs_cache_reserve", dev, _ptr(table), _ptr(refs), _ptr(lens), _ptr(want), _ptr(src),
           _ptr(dst), c, _ptr(ws), need)
@@ -383,7 +393,7 @@ def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.
         _ints(mask, "mask", (c.seqs, tree, (tree + 31) // 32), dev)
     zero = count is not None and out is None
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = _fresh(q)
     else:
         _on(out, "out", dev)
         if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
