@@ -30,14 +30,17 @@ struct MmaCfg {
   static constexpr int H = D / 64;
   static constexpr int ROWS = 16;
   static constexpr uint32_t KV = kKeys * D * 2;   // bytes of a K or V tile
-  static constexpr int ST = D == 128 ? 4 : 8;     // even: a stage stays with one half
+  // 192 KB in flight an SM (128 KB: 6 % slower on a ragged batch, 64 KB: 30 %);
+  // even: a stage stays with one half
+  static constexpr int ST = D == 128 ? 6 : 12;
+  static constexpr int RJ = 4;                    // rows joined at a time
   static constexpr int PAD = 4;                   // floats behind a joined row
-  static constexpr size_t JOIN = (size_t)kConsumers * 16 * (D + PAD) * 4;
+  static constexpr size_t JOIN = (size_t)kConsumers * RJ * (D + PAD) * 4;
   struct Bars {
     uint64_t full[ST], empty[ST], join;
     int abort, bad;
     float2 ml[kConsumers][ROWS];
-    Place place;
+    int sum[kConsumers + 1];
   };
   static constexpr size_t SMEM = 1024 + 2 * KV * ST + ROWS * D * 2 + JOIN + sizeof(Bars);
 };
@@ -65,8 +68,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     fence_barrier_init();
   }
   allow_next();
-  if (!find_place<ROWS, kKeys, kMmaThreads>(a, &bar->place)) return;
-  Walk<ROWS, kKeys> walk(bar->place);
+  __syncthreads();
+  Place place;
+  if (!find_place<ROWS, kKeys, kMmaThreads>(a, bar->sum, &place)) return;
+  Walk<ROWS, kKeys> walk(place);
   Segment g;
 
   if (warp == kConsumers) {
@@ -239,18 +244,25 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
         const int row = key16 + (lane & 15);
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          const int ch = n * 2 + (lane >> 4);
-          uint32_t b[4];
-          ldsm_x4_t(b, tV + (ch >> 3) * (kKeys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-          if (edge) {
+        for (int n = 0; n < D / 16; n += 2) {
+          uint32_t b[2][4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) b[x] = clean2<T>(b[x], keep[x & 1], drafted[x & 1], &bad);
+          for (int y = 0; y < 2; ++y) {
+            const int ch = (n + y) * 2 + (lane >> 4);
+            ldsm_x4_t(b[y],
+                      tV + (ch >> 3) * (kKeys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            if (edge) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                b[y][x] = clean2<T>(b[y][x], keep[x & 1], drafted[x & 1], &bad);
+            }
           }
-          Two<T>::mma(o[2 * n], hi, b[0], b[1]);
-          Two<T>::mma(o[2 * n + 1], hi, b[2], b[3]);
-          Two<T>::mma(o[2 * n], lo, b[0], b[1]);
-          Two<T>::mma(o[2 * n + 1], lo, b[2], b[3]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            Two<T>::mma(o[2 * n + y], hi, b[y >> 1][2 * (y & 1)], b[y >> 1][2 * (y & 1) + 1]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            Two<T>::mma(o[2 * n + y], lo, b[y >> 1][2 * (y & 1)], b[y >> 1][2 * (y & 1) + 1]);
         }
       }
       warp_arrive(&bar->empty[st], lane);
@@ -264,56 +276,55 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       t += __shfl_xor_sync(0xffffffffu, t, 2);
       if ((lane & 3) == 0) bar->ml[warp][gr + 8 * x] = make_float2(m[x], t);
     }
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    const int slot = 2 * blockIdx.x + (seg > 0);
+    constexpr int RJ = C::RJ, N = D * RJ / (32 * kConsumers);  // columns a thread joins
+    for (int r0 = 0; r0 < rows; r0 += RJ) {
 #pragma unroll
       for (int x = 0; x < 2; ++x)
-        if (gr + 8 * x < rows)
-          *reinterpret_cast<float2 *>(join + (warp * 16 + gr + 8 * x) * (D + C::PAD) + n * 8 + qc) =
-              make_float2(o[n][2 * x], o[n][2 * x + 1]);
-    if (!sync()) return;
-    const int slot = 2 * blockIdx.x + (seg > 0);
-    constexpr int N = D / 16;  // columns a thread joins: 16 threads a row
-    const int r = tid & 15, col = (tid >> 4) * N;
-    if (r < rows) {
-      float top = -INFINITY;
+        if ((unsigned)(gr + 8 * x - r0) < RJ) {
+          float *dst = join + (warp * RJ + gr + 8 * x - r0) * (D + C::PAD) + qc;
 #pragma unroll
-      for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, bar->ml[w][r].x);
-      float sum = 0.f, acc[N];
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
+        }
+      if (!sync()) return;
+      const int r = r0 + tid % RJ, col = tid / RJ * N;
+      if (r < rows) {
+        float top = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < N; ++e) acc[e] = 0.f;
+        for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, bar->ml[w][r].x);
+        float sum = 0.f, acc[N];
 #pragma unroll
-      for (int w = 0; w < kConsumers; ++w) {
-        const float2 ml = bar->ml[w][r];
-        const float f = part_scale(ml.x, top);
-        const float *src = join + (w * 16 + r) * (D + C::PAD) + col;
-        sum += ml.y * f;
+        for (int e = 0; e < N; ++e) acc[e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < N; e += 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(src + e);
-          acc[e] += v.x * f, acc[e + 1] += v.y * f;
-          acc[e + 2] += v.z * f, acc[e + 3] += v.w * f;
+        for (int w = 0; w < kConsumers; ++w) {
+          const float2 ml = bar->ml[w][r];
+          const float f = part_scale(ml.x, top);
+          const float *src = join + (w * RJ + r - r0) * (D + C::PAD) + col;
+          sum += ml.y * f;
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] += src[e] * f;
+        }
+        const int rr = g.rt * ROWS + r;
+        if (g.whole) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] *= inv;
+          if (*(volatile int *)&bar->bad)
+            add_wild<T, N>(a, g.s, g.h, Seq{g.start, g.count}, rr / a.G, D, col, acc);
+          write_row<T, N>(a, g.s, g.h, rr, D, col, acc);
+          if (col == 0) write_lse(a, g.s, g.h, rr, top, sum);
+        } else {
+          float *dst = reinterpret_cast<float *>(
+              a.part_o + ((size_t)slot * (D / 4) + col / 4) * ROWS + r) + col % 4;
+#pragma unroll
+          for (int e = 0; e < N; ++e) dst[e] = acc[e];
+          if (col == 0) a.part_ml[(size_t)slot * ROWS + r] = make_float2(top, sum);
+          if (tid == 0 && r0 == 0) a.part_bad[slot] = *(volatile int *)&bar->bad;
         }
       }
-      const int rr = g.rt * ROWS + r;
-      if (g.whole) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] *= inv;
-        if (*(volatile int *)&bar->bad)
-          add_wild<T, N>(a, g.s, g.h, Seq{g.start, g.count}, rr / a.G, D, col, acc);
-        write_row<T, N>(a, g.s, g.h, rr, D, col, acc);
-        if (col == 0) write_lse(a, g.s, g.h, rr, top, sum);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; e += 4)
-          a.part_o[((size_t)slot * (D / 4) + (col + e) / 4) * ROWS + r] =
-              make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-        if (col == 0) a.part_ml[(size_t)slot * ROWS + r] = make_float2(top, sum);
-        if (tid == 0) a.part_bad[slot] = *(volatile int *)&bar->bad;
-      }
+      if (!sync()) return;  // the join buffer (behind the last rows, Q too) is free again
     }
-    if (!sync()) return;  // the join buffer and Q are free again
   }
 }
 

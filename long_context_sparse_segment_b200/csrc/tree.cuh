@@ -80,60 +80,54 @@ struct Runs {
 };
 
 // The place of a CTA's run: its first and end unit, and the sequence that the
-// first lies in with the units before that one. Filled once per CTA.
+// first lies in with the units before that one.
 struct Place {
   int u0, u1, s, before;
-  int sum[17];
 };
 
 // Every thread of the block (NT of them, a multiple of 32) calls it; false
-// for a CTA without units. Ends with a barrier where it returns true.
+// for a CTA without units. `sum`: NT / 32 words of shared memory.
 template <int ROWS, int KEYS, int NT>
-__device__ __forceinline__ bool find_place(const TreeArgs &a, Place *p) {
+__device__ __forceinline__ bool find_place(const TreeArgs &a, int *sum, Place *p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto units = [&](int s) { return s < a.seqs ? units_of<ROWS, KEYS>(a, seq_of(a, s)) : 0; };
-  // up to 32 sequences every warp holds them all; more are summed by the block
-  // first (one more barrier and a second look at the lengths: 0.7 us more)
-  int x = units(a.seqs <= 32 ? lane : tid), sum = x, total = 0;
-  if (a.seqs > 32)
-    for (int s = tid + NT; s < a.seqs; s += NT) sum += units(s);
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  if (a.seqs <= 32) {
-    total = sum;
-  } else {
-    if (lane == 0) p->sum[warp] = sum;
+  // up to 32 sequences a warp holds them all and nobody waits for another; more
+  // are summed by the block first
+  int x = units(a.seqs <= 32 ? lane : tid), total = x;
+  if (a.seqs > 32) {
+    for (int s = tid + NT; s < a.seqs; s += NT) total += units(s);
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (lane == 0) sum[warp] = total;
     __syncthreads();
+    total = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) total += p->sum[w];
+    for (int w = 0; w < NT / 32; ++w) total += sum[w];
+    x = units(lane);
+  } else {
+    total = __reduce_add_sync(0xffffffffu, total);
   }
   const int runs = min(total, (int)gridDim.x);
   if ((int)blockIdx.x >= runs) return false;
   const Runs run(total, runs);
-  const int u0 = run.start(blockIdx.x);
-  if (warp == 0) {
-    int base = 0;
-    for (int s0 = 0;; s0 += 32) {
-      if (s0 > 0) x = units(s0 + lane);
-      int inc = x;
+  p->u0 = run.start(blockIdx.x), p->u1 = run.start(blockIdx.x + 1);
+  int base = 0;
+  for (int s0 = 0;; s0 += 32) {
+    if (s0 > 0) x = units(s0 + lane);
+    int inc = x;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      inc += base;
-      const unsigned m = __ballot_sync(0xffffffffu, inc > u0);
-      if (m) {
-        if (lane == __ffs(m) - 1) {
-          p->u0 = u0, p->u1 = run.start(blockIdx.x + 1);
-          p->s = s0 + lane, p->before = inc - x;
-        }
-        break;
-      }
-      base = __shfl_sync(0xffffffffu, inc, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
+    inc += base;
+    const unsigned m = __ballot_sync(0xffffffffu, inc > p->u0);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      p->s = s0 + l, p->before = __shfl_sync(0xffffffffu, inc - x, l);
+      return true;
+    }
+    base = __shfl_sync(0xffffffffu, inc, 31);
   }
-  __syncthreads();
-  return true;
 }
 
 // A piece of a CTA's run inside one item.
@@ -219,8 +213,7 @@ struct Two<__half> {
   static constexpr uint32_t kExp = 0x7c00u;
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
         "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -231,6 +224,15 @@ struct Two<__half> {
 template <typename T>
 __device__ __forceinline__ bool wild16(uint32_t x) {
   return (x & Two<T>::kExp) == Two<T>::kExp;
+}
+
+// Nonzero when a half of u is NaN or infinite: the exponent's all-ones carries
+// into the sign's place.
+template <typename T>
+__device__ __forceinline__ uint32_t wild2(uint32_t u) {
+  constexpr uint32_t e = Two<T>::kExp * 0x10001u;
+  constexpr uint32_t one = (0x8000u - Two<T>::kExp) * 0x10001u;
+  return ((u & e) + one) & 0x80008000u;
 }
 
 // The two halves of u that `keep` (bits 0, 1) has; with `drafted` (bits 0, 1)
@@ -270,7 +272,11 @@ __device__ __forceinline__ void write_row(const TreeArgs &a, int s, int h, int r
                                           const float (&o)[N]) {
   const int i = r / a.G, g = r % a.G;
   T *dst = (T *)a.out + (((size_t)s * a.hq + h * a.G + g) * a.tree + i) * d + col;
-  uint32_t p[N / 2];
+  if constexpr (N == 1) {
+    *reinterpret_cast<uint16_t *>(dst) = (uint16_t)Two<T>::pack(o[0], 0.f);
+    return;
+  }
+  uint32_t p[N / 2 + 1];
 #pragma unroll
   for (int e = 0; e < N / 2; ++e) p[e] = Two<T>::pack(o[2 * e], o[2 * e + 1]);
   if constexpr (N == 8)
@@ -343,7 +349,10 @@ __global__ void __launch_bounds__(kCombineThreads)
     if (wc == 0 && a.lse)
       a.lse[((size_t)s * a.hq + h * a.G + wr % a.G) * a.tree + wr / a.G] = 0.f;
   }
-  if (r0 >= rows) return;
+  if (r0 >= rows) {
+    wait_previous();
+    return;
+  }
   // units before this sequence, and all
   int mine = 0, all = 0;
   for (int i = tid; i < a.seqs; i += kCombineThreads) {
@@ -363,9 +372,9 @@ __global__ void __launch_bounds__(kCombineThreads)
   u0 += (h * rts + r0 / ROWS) * kt;
   const Runs run(total, min(total, grid));
   const int c0 = run.owner(u0), c1 = run.owner(u0 + kt - 1);
-  if (c0 == c1) return;
   const int slot0 = 2 * c0 + (run.start(c0) != u0);
-  wait_previous();
+  wait_previous();  // on every path, so that this kernel never ends before the other
+  if (c0 == c1) return;
   const int r = tid % RB, c4 = tid / RB % C4, pg = tid / (RB * C4);
   const bool live = r0 + r < rows;
   Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};

@@ -45,7 +45,7 @@ struct Cfg {
   static constexpr int ROWS = PAIR ? 256 : 128;
   static constexpr uint32_t TILE = kTile * D * 2, HALF = kTile * 128;
   static constexpr int PARTS = PAIR ? 1 : kSingleParts;  // 16-bit parts of P
-  static constexpr int KS = D == 128 ? 2 : 5, VS = D == 128 ? 3 : 5;
+  static constexpr int KS = D == 64 ? 5 : 2, VS = D == 64 ? 5 : 3;
   static_assert(VS + 2 < kBadSlots, "bad flags");
   struct Shared {
     uint64_t q_full, seg, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], v_clean[VS], s_full[2],
@@ -53,13 +53,15 @@ struct Cfg {
     uint32_t tmem;
     int abort;
     int bad[kBadSlots][2];  // by warp
+    int sum[kThreads / 32];
     Place place;
-    float2 ml[2][PAIR ? 1 : kTile];
   };
   static constexpr size_t SMEM =
       1024 + (size_t)(ROWS / kTile + KS + VS) * TILE + sizeof(Shared);
 };
-static_assert(Cfg<128, true>::SMEM <= 232448 && Cfg<64, true>::SMEM <= 232448, "shared memory");
+static_assert(Cfg<128, true>::SMEM <= 232448 && Cfg<128, false>::SMEM <= 232448 &&
+                  Cfg<64, true>::SMEM <= 232448,
+              "shared memory");
 
 // Instruction descriptor, kind::f16, fp32 accumulator; A and B of type T.
 template <typename T>
@@ -71,6 +73,16 @@ __host__ __device__ constexpr uint32_t idesc16<__nv_bfloat16>(int m, int n, bool
 template <>
 __host__ __device__ constexpr uint32_t idesc16<__half>(int m, int n, bool b) {
   return idesc_bf16(m, n, b) & ~((1u << 7) | (1u << 10));
+}
+
+// A 16-byte word of V without its NaN and infinities. Out of line: it hardly
+// ever runs, and code that runs once an item is paid for in instruction fetches.
+template <typename T>
+__device__ __noinline__ void clean_word(uint4 *p) {
+  bool bad = false;
+  const uint4 v = *p;
+  *p = make_uint4(clean2<T>(v.x, 3, 3, &bad), clean2<T>(v.y, 3, 3, &bad),
+                  clean2<T>(v.z, 3, 3, &bad), clean2<T>(v.w, 3, 3, &bad));
 }
 
 template <typename T, int D, bool PAIR>
@@ -112,15 +124,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   allow_next();
   tc_fence_before();
-  // its last barrier publishes the initialisation
-  if (!find_place<ROWS, kTile, kThreads>(a, &sh->place)) {
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 1) tmem_dealloc(sh->tmem, 512);
-    return;
-  }
+  __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sh->tmem;
+  {
+    Place place;
+    if (!find_place<ROWS, kTile, kThreads>(a, sh->sum, &place)) {
+      if (warp == 1) tmem_dealloc(tbase, 512);
+      return;
+    }
+    if (tid == 0) sh->place = place;
+  }
+  __syncthreads();
   Walk<ROWS, kTile> walk(sh->place);
   Segment g{};
   if (warp < 4) {
@@ -299,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((k + 1) * kTile > g.start) {
             uint8_t *tile = sV + (size_t)st * C::TILE;
             const int first = max(0, g.start - k * kTile), len = g.start + g.count - k * kTile;
-            bool bad = false;
+#pragma unroll 1
             for (int x = t64; x < (kTile - first) * (D / 8); x += 64) {
               const int row = first + x / (D / 8), ch = x % (D / 8);
               uint4 *p = reinterpret_cast<uint4 *>(tile + (ch >> 3) * C::HALF + row * 128 +
@@ -308,13 +323,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *p = make_uint4(0, 0, 0, 0);
               } else {
                 const uint4 v = *p;
-                bool hit = false;
-                const uint4 w = make_uint4(clean2<T>(v.x, 3, 3, &hit), clean2<T>(v.y, 3, 3, &hit),
-                                           clean2<T>(v.z, 3, 3, &hit), clean2<T>(v.w, 3, 3, &hit));
-                if (hit) *p = w, bad = true;
+                if (wild2<T>(v.x) | wild2<T>(v.y) | wild2<T>(v.z) | wild2<T>(v.w)) {
+                  clean_word<T>(p);
+                  *flag = 1;
+                }
               }
             }
-            if (bad) *flag = 1;
             fence_proxy_async_smem();
           }
           warp_arrive(&sh->v_clean[st], lane);
@@ -481,15 +495,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rr = g.rt * ROWS + row;
     float top = m_used, sum = l, f[2] = {1.f, 1.f};
     if (!PAIR) {
-      // both streams' outputs, half of the columns by each group of warps
-      sh->ml[x][lrow] = make_float2(m_used, l);
-      ok = seg_sync();
+      // both streams' outputs, half of the columns by each group of warps;
+      // the products are through with Q, whose place takes the sums
       for (int y = 0; y < 2 && ok; ++y)
         if (y == 0 || n > 1) {
           ok = mbar_wait_warp(&sh->o_final[y], o_phase >> y & 1, abort, a.err, 44);
           o_phase ^= 1u << y;
         }
-      const float2 p0 = sh->ml[0][lrow], p1 = sh->ml[1][lrow];
+      if (!ok) break;
+      float2 *ml = reinterpret_cast<float2 *>(sQ);  // [2][kTile]
+      ml[x * kTile + lrow] = make_float2(m_used, l);
+      ok = seg_sync();
+      const float2 p0 = ml[lrow], p1 = ml[kTile + lrow];
       top = fmaxf(p0.x, p1.x);
       f[0] = part_scale(p0.x, top), f[1] = n > 1 ? part_scale(p1.x, top) : 0.f;
       sum = p0.y * f[0] + (n > 1 ? p1.y * f[1] : 0.f);
