@@ -13,15 +13,16 @@
 // integers, modulo 2^64, is the angle modulo one turn without rounding, and
 // its upper 32 bits go through sincospif. What is left is f's own rounding
 // (2^-53 relative, times t) and fp32's 2^-24 of half a turn.
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "decode.h"
-
-#include <cuda_fp16.h>
 
 namespace pbs {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int kHeads = 4;  // heads whose reads are in flight together
 
 struct RopeArgs {
   pbs_rows q, qo, k, ko;
@@ -73,6 +74,30 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4], float) {
                     __float_as_uint(x[3]));
 }
 
+// The V pairs of two vectors turned by their angles. HALF: pair e is element e
+// of each; else elements 2e and 2e + 1 of the two together.
+template <typename T, bool HALF, int V>
+__device__ __forceinline__ void turn(uint4 &v0, uint4 &v1, const float (&c)[V],
+                                     const float (&s)[V]) {
+  float x0[V], x1[V], y0[V], y1[V];
+  unpack(v0, x0, T());
+  unpack(v1, x1, T());
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    if (HALF) {
+      y0[e] = x0[e] * c[e] - x1[e] * s[e];
+      y1[e] = x1[e] * c[e] + x0[e] * s[e];
+    } else {
+      const float p = 2 * e < V ? x0[2 * e % V] : x1[2 * e % V];
+      const float r = 2 * e < V ? x0[2 * e % V + 1] : x1[2 * e % V + 1];
+      (2 * e < V ? y0 : y1)[2 * e % V] = p * c[e] - r * s[e];
+      (2 * e < V ? y0 : y1)[2 * e % V + 1] = r * c[e] + p * s[e];
+    }
+  }
+  v0 = pack(y0, T());
+  v1 = pack(y1, T());
+}
+
 // A unit is two 16-byte vectors of a head's row. HALF: a rotated unit u
 // holds elements [uV, uV + V) and the same from rot/2 on; else the 2V
 // elements from 2uV on, V pairs side by side. Units behind rot are copied.
@@ -103,36 +128,33 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     }
   }
   const int h0 = blockIdx.y * a.heads_per, h1 = min(h0 + a.heads_per, a.heads);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const bool is_q = h < a.hq;
-    const pbs_rows &x = is_q ? a.q : a.k, &y = is_q ? a.qo : a.ko;
-    const int hh = is_q ? h : h - a.hq;
-    const T *src = (const T *)x.p + b * x.batch + hh * x.head + i * x.row;
-    T *dst = (T *)y.p + b * y.batch + hh * y.head + i * y.row;
-    uint4 v0 = *reinterpret_cast<const uint4 *>(src + lo);
-    uint4 v1 = *reinterpret_cast<const uint4 *>(src + hi);
-    if (turns) {
-      float x0[V], x1[V], y0[V], y1[V];
-      unpack(v0, x0, T());
-      unpack(v1, x1, T());
+  // the q heads of this block's share, then the k heads
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const pbs_rows &x = part ? a.k : a.q, &y = part ? a.ko : a.qo;
+    const int off = part ? a.hq : 0;
+    const int first = max(h0, off) - off, end = (part ? h1 : min(h1, a.hq)) - off;
+    const T *src = (const T *)x.p + b * x.batch + i * x.row;
+    T *dst = (T *)y.p + b * y.batch + i * y.row;
+#pragma unroll 1
+    for (int h = first; h < end; h += kHeads) {
+      uint4 v0[kHeads], v1[kHeads];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (HALF) {
-          y0[e] = x0[e] * c[e] - x1[e] * s[e];
-          y1[e] = x1[e] * c[e] + x0[e] * s[e];
-        } else {  // pair e: elements 2e, 2e + 1 of the unit's 2V
-          const float p = 2 * e < V ? x0[2 * e % V] : x1[2 * e % V];
-          const float r = 2 * e < V ? x0[2 * e % V + 1] : x1[2 * e % V + 1];
-          (2 * e < V ? y0 : y1)[2 * e % V] = p * c[e] - r * s[e];
-          (2 * e < V ? y0 : y1)[2 * e % V + 1] = r * c[e] + p * s[e];
+      for (int e = 0; e < kHeads; ++e)
+        if (h + e < end) {
+          const T *p = src + (h + e) * x.head;
+          v0[e] = *reinterpret_cast<const uint4 *>(p + lo);
+          v1[e] = *reinterpret_cast<const uint4 *>(p + hi);
         }
-      }
-      v0 = pack(y0, T());
-      v1 = pack(y1, T());
+#pragma unroll
+      for (int e = 0; e < kHeads; ++e)
+        if (h + e < end) {
+          if (turns) turn<T, HALF>(v0[e], v1[e], c, s);
+          T *p = dst + (h + e) * y.head;
+          *reinterpret_cast<uint4 *>(p + lo) = v0[e];
+          *reinterpret_cast<uint4 *>(p + hi) = v1[e];
+        }
     }
-    *reinterpret_cast<uint4 *>(dst + lo) = v0;
-    *reinterpret_cast<uint4 *>(dst + hi) = v1;
   }
 }
 
@@ -167,9 +189,9 @@ extern "C" pbs_status pbs_rope(pbs_rows q, pbs_rows q_out, int hq, pbs_rows k, p
   a.hq = hq, a.heads = hq + hkv, a.n = n, a.d = d, a.rot = rot, a.transpose = transpose != 0;
   const int64_t bx = ceil_div(a.tokens * (d * elem / 32), kThreads);
   if (bx > 0x7fffffff) return PBS_ERR_UNSUPPORTED;
-  // few tokens: the heads are split over blocks until there are eight blocks
+  // few tokens: the heads are split over blocks until there are sixteen blocks
   // an SM, and the angles computed again in each
-  int64_t split = ceil_div(148 * 8, bx);
+  int64_t split = ceil_div(148 * 16, bx);
   if (split > a.heads) split = a.heads;
   a.heads_per = (int)ceil_div(a.heads, split);
   if (ceil_div(a.heads, a.heads_per) > 65535) return PBS_ERR_UNSUPPORTED;

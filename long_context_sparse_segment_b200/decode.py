@@ -52,6 +52,12 @@ def _ints(t, name, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _dense(t):
+    """A contiguous [b, h, n, d] as pbs_rows."""
+    _, h, n, d = t.shape
+    return Rows(t.data_ptr(), 0, h * n * d, n * d, d)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -192,9 +198,11 @@ def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=No
     if b and n and hq + hkv:
         qr = kr = qo = ko = _NONE
         if hq:
-            qr, qo = _rows(q, "q"), _rows(outs[0], "q_out", q_out is not None)
+            qr = _rows(q, "q")
+            qo = _dense(outs[0]) if q_out is None else _rows(q_out, "q_out", True)
         if hkv:
-            kr, ko = _rows(k, "k"), _rows(outs[1], "k_out", k_out is not None)
+            kr = _rows(k, "k")
+            ko = _dense(outs[1]) if k_out is None else _rows(k_out, "k_out", True)
         _call("pbs_rope", dev, qr, qo, hq, kr, ko, hkv, _ptr(pos), 0 if pos.dim() == 1 else n,
               _ptr(inv_freq), gain, b, n, d, rot, _LAYOUTS[layout], int(bool(transpose)),
               _TYPES[q.dtype])
