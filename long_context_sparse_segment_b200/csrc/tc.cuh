@@ -13,6 +13,10 @@ namespace pbs {
 // the driver's encoder is unavailable or rejects the arguments.
 bool make_tile_map(CUtensorMap *map, const void *ptr, uint64_t rows, int d, int box_rows);
 
+// The same rows as a 3-D map (64 columns, rows, d / 64 column halves): one copy
+// brings whole rows, the halves one behind the other.
+bool make_tile_map_halves(CUtensorMap *map, const void *ptr, uint64_t rows, int d, int box_rows);
+
 namespace tc {
 
 // Bounded waits: a wait that has not completed after this long records
@@ -165,6 +169,14 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 // One arrival on the mbarrier once every cp.async this thread has issued so

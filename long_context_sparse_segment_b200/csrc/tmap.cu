@@ -44,4 +44,18 @@ bool make_tile_map(CUtensorMap *map, const void *ptr, uint64_t rows, int d, int 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tile_map_halves(CUtensorMap *map, const void *ptr, uint64_t rows, int d, int box_rows) {
+  EncodeTiled enc = encode_fn();
+  if (!enc || box_rows < 1 || box_rows > 256) return false;
+  const cuuint32_t halves = (cuuint32_t)d / 64;
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, halves};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, halves};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pbs

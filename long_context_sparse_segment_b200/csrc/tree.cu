@@ -37,12 +37,14 @@ struct MmaCfg {
   static constexpr int PAD = 4;                   // floats behind a joined row
   static constexpr size_t JOIN = (size_t)kConsumers * RJ * (D + PAD) * 4;
   struct Bars {
-    uint64_t full[ST], empty[ST], join;
-    int abort, bad;
+    uint64_t full[ST], empty[ST], q_full[2], q_empty[2], join;
+    int abort;
+    int bad[kConsumers];
+    Segment g[2];
     float2 ml[kConsumers][ROWS];
     int sum[kConsumers + 1];
   };
-  static constexpr size_t SMEM = 1024 + 2 * KV * ST + ROWS * D * 2 + JOIN + sizeof(Bars);
+  static constexpr size_t SMEM = 1024 + 2 * KV * ST + 2 * ROWS * D * 2 + JOIN + sizeof(Bars);
 };
 static_assert(MmaCfg<128>::SMEM <= 232448 && MmaCfg<64>::SMEM <= 232448, "shared memory");
 
@@ -56,66 +58,92 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   uint8_t *base = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *ring = base;                          // [ST][K tile, V tile]
-  T *sQ = reinterpret_cast<T *>(ring + 2 * C::KV * ST);
-  float *join = reinterpret_cast<float *>(sQ + ROWS * D);
+  T *sQ = reinterpret_cast<T *>(ring + 2 * C::KV * ST);  // [2][ROWS][D]
+  float *join = reinterpret_cast<float *>(sQ + 2 * ROWS * D);
   auto *bar = reinterpret_cast<typename C::Bars *>(reinterpret_cast<uint8_t *>(join) + C::JOIN);
   volatile int *abort = &bar->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) mbar_init(&bar->full[i], 1), mbar_init(&bar->empty[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->q_full[i], 33);  // each lane's copies, and the segment
+      mbar_init(&bar->q_empty[i], kConsumers);
+    }
     mbar_init(&bar->join, kConsumers);
-    bar->abort = 0, bar->bad = 0;
+    bar->abort = 0;
     fence_barrier_init();
   }
   allow_next();
   __syncthreads();
   Place place;
   if (!find_place<ROWS, kKeys, kMmaThreads>(a, bar->sum, &place)) return;
-  Walk<ROWS, kKeys> walk(place);
-  Segment g;
+  // a tile in shared memory: [piece of a page][64-column half][row][128 bytes]
+  const int box = min(a.page, kKeys);
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------- producer
-    // A unit is up to 4 boxes of page rows x 64 columns, H column halves, K
-    // and V: one lane each. Rows of a page behind the last token come along;
-    // pages behind it do not.
-    const int box = min(a.page, kKeys), pieces = kKeys / box;
-    const int kv = lane & 1, half = (lane >> 1) % H, piece = (lane >> 1) / H;
-    const bool mine = piece < pieces;
-    int it = 0;
-    bool ok = true;
+    // Finds the segments, brings each one's Q rows (a segment ahead of the
+    // consumers, as the ring allows) and its units: up to 4 pieces of pages,
+    // K and V, one lane each. Rows of a page behind the last token come along;
+    // pages behind it do not. A unit's page numbers are read one unit early.
+    Walk<ROWS, kKeys> walk(place);
+    Segment g;
+    const int kv = lane & 1, piece = lane >> 1, shift = 31 - __clz(a.page);
+    const bool mine = piece < kKeys / box;
+    int it = 0, seg = 0;
     if (lane == 0) prefetch_map(&tmK), prefetch_map(&tmV);
-    while (ok && walk.next(a, &g)) {
+    for (bool more = true, ok = true; more && ok; ++seg) {
+      more = walk.next(a, &g);
+      const int slot = seg & 1;
+      if (seg >= 2 && !mbar_wait_warp(&bar->q_empty[slot], (seg / 2 - 1) & 1, abort, a.err, 12))
+        break;
+      if (lane == 0) {
+        if (!more) g.count = 0;  // the end
+        bar->g[slot] = g;
+        mbar_arrive(&bar->q_full[slot]);
+      }
+      if (more) {
+        const int n = min(ROWS, g.count * a.G - g.rt * ROWS) * (D / 8);
+        for (int x = lane; x < n; x += 32) {  // rows behind: anything
+          const int r = x / (D / 8), ch = x % (D / 8);
+          const int rr = g.rt * ROWS + r, i = rr / a.G, hd = g.h * a.G + rr - i * a.G;
+          cp_async16(sQ + slot * ROWS * D + swz<D>(r, ch * 8),
+                     (const T *)a.q.p + (int64_t)g.s * a.q.batch + hd * a.q.head + i * a.q.row +
+                         ch * 8);
+        }
+      }
+      cp_async_mbar_arrive(&bar->q_full[slot]);
+      if (!more) break;
       const int len = g.start + g.count;
       const int32_t *row = a.table + (size_t)g.s * a.width;
-      for (int k = g.k0; k < g.k1; ++k, ++it) {
+      int t = g.k0 * kKeys + piece * box;
+      auto page_of = [&](int tok) { return mine && tok < len ? __ldg(row + (tok >> shift)) : 0; };
+      int page = page_of(t);
+      for (int k = g.k0; k < g.k1; ++k, ++it, t += kKeys) {
         const int st = it % ST;
-        const int t = k * kKeys + piece * box;
         const bool load = mine && t < len;
-        int y = 0;
-        if (load) {
-          int page = __ldg(row + t / a.page);
-          if (page < 0 || page >= a.pages) {
-            report(a.err, PBS_ERR_DEVICE_ASSERT);
-            page = 0;
-          }
-          y = (page * a.hkv + g.h) * a.page + t % a.page;
+        const int ahead = k + 1 < g.k1 ? page_of(t + kKeys) : 0;
+        if (load && (page < 0 || page >= a.pages)) {
+          report(a.err, PBS_ERR_DEVICE_ASSERT);
+          page = 0;
         }
+        const int y = (page * a.hkv + g.h) * a.page + (t & (a.page - 1));
         const int boxes = __popc(__ballot_sync(0xffffffffu, load));
         if (it >= ST && !mbar_wait_warp(&bar->empty[st], (it / ST - 1) & 1, abort, a.err, 11)) {
           ok = false;
           break;
         }
-        if (lane == 0) mbar_expect_tx(&bar->full[st], boxes * box * 128);
+        if (lane == 0) mbar_expect_tx(&bar->full[st], boxes * box * D * 2);
         __syncwarp();
         if (load)
-          tma_load_2d(ring + (size_t)(2 * st + kv) * C::KV + half * (kKeys * 128) +
-                          piece * box * 128,
-                      kv ? &tmV : &tmK, &bar->full[st], half * 64, y);
+          tma_load_3d(ring + (size_t)(2 * st + kv) * C::KV + piece * box * D * 2,
+                      kv ? &tmV : &tmK, &bar->full[st], 0, y, 0);
         __syncwarp();
+        page = ahead;
       }
     }
     // every copy started here lands before the CTA exits
+    cp_async_wait_all();
     int never = 0;
     for (int i = it > ST ? it - ST : 0; i < it; ++i)
       mbar_wait(&bar->full[i % ST], (i / ST) & 1, &never, nullptr);
@@ -132,30 +160,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     phase ^= 1;
     return ok;
   };
+  const uint32_t half_bytes = box * 128;  // from one column half to the other
+  const uint32_t key_bytes = key16 / box * (box * D * 2) + key16 % box * 128;
   int it = 0;
-  for (int seg = 0; walk.next(a, &g); ++seg) {
+  for (int seg = 0;; ++seg) {
+    if (!mbar_wait_warp(&bar->q_full[seg & 1], seg >> 1 & 1, abort, a.err, 42)) return;
+    const Segment g = bar->g[seg & 1];
+    if (g.count == 0) return;
     const int rows = min(ROWS, g.count * a.G - g.rt * ROWS);  // of this row tile
     const int len = g.start + g.count;
-    // Q rows into shared memory, 16-byte chunks XOR-swizzled by row
-    for (int x = tid; x < ROWS * (D / 8); x += 32 * kConsumers) {
-      const int r = x / (D / 8), ch = x % (D / 8);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const int rr = g.rt * ROWS + r, i = rr / a.G, hd = g.h * a.G + rr % a.G;
-        v = *reinterpret_cast<const uint4 *>((const T *)a.q.p + (int64_t)g.s * a.q.batch +
-                                             hd * a.q.head + i * a.q.row + ch * 8);
-      }
-      *reinterpret_cast<uint4 *>(sQ + swz<D>(r, ch * 8)) = v;
-    }
-    if (tid == 0) bar->bad = 0;
-    if (!sync()) return;
     int draft[2];  // of this thread's rows
 #pragma unroll
     for (int x = 0; x < 2; ++x) draft[x] = min((g.rt * ROWS + gr + 8 * x) / a.G, g.count - 1);
     uint32_t q[D / 16][4];
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
-      ldsm_x4(q[kk], sQ + swz<D>(lane & 15, kk * 16 + ((lane >> 4) << 3)));
+      ldsm_x4(q[kk], sQ + (seg & 1) * ROWS * D + swz<D>(lane & 15, kk * 16 + ((lane >> 4) << 3)));
+    warp_arrive(&bar->q_empty[seg & 1], lane);
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
@@ -166,7 +187,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       if ((it & 1) != half_id) continue;
       const int st = it % ST;
       if (!mbar_wait_warp(&bar->full[st], (it / ST) & 1, abort, a.err, 41)) return;
-      const uint8_t *tK = ring + (size_t)(2 * st) * C::KV, *tV = tK + C::KV;
+      const uint8_t *tK = ring + (size_t)(2 * st) * C::KV + key_bytes, *tV = tK + C::KV;
       const int key0 = k * kKeys + key16;  // this warp's 16 keys
       if (key0 < len) {
         // S = Q K^T
@@ -176,12 +197,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
         {
-          const int row = key16 + (lane & 7) + ((lane >> 4) << 3);
+          const int row = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const int ch = kk * 2 + ((lane >> 3) & 1);
             uint32_t b[4];
-            ldsm_x4(b, tK + (ch >> 3) * (kKeys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            ldsm_x4(b, tK + (ch >> 3) * half_bytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
             Two<T>::mma(s[0], q[kk], b[0], b[1]);
             Two<T>::mma(s[1], q[kk], b[2], b[3]);
           }
@@ -242,7 +263,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             drafted[x] = (t >= g.start) | (t + 1 >= g.start) << 1;
           }
         }
-        const int row = key16 + (lane & 15);
+        const int row = lane & 15;
 #pragma unroll
         for (int n = 0; n < D / 16; n += 2) {
           uint32_t b[2][4];
@@ -250,7 +271,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           for (int y = 0; y < 2; ++y) {
             const int ch = (n + y) * 2 + (lane >> 4);
             ldsm_x4_t(b[y],
-                      tV + (ch >> 3) * (kKeys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+                      tV + (ch >> 3) * half_bytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
             if (edge) {
 #pragma unroll
               for (int x = 0; x < 4; ++x)
@@ -268,17 +289,28 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       warp_arrive(&bar->empty[st], lane);
     }
     // ------------------------------------------------ join the eight warps
-    if (__any_sync(0xffffffffu, bad) && lane == 0) bar->bad = 1;
+    bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      float t = l[x];
-      t += __shfl_xor_sync(0xffffffffu, t, 1);
-      t += __shfl_xor_sync(0xffffffffu, t, 2);
-      if ((lane & 3) == 0) bar->ml[warp][gr + 8 * x] = make_float2(m[x], t);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
     }
     const int slot = 2 * blockIdx.x + (seg > 0);
     constexpr int RJ = C::RJ, N = D * RJ / (32 * kConsumers);  // columns a thread joins
+    auto any_bad = [&]() {
+      int x = 0;
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) x |= bar->bad[w];
+      return x;
+    };
     for (int r0 = 0; r0 < rows; r0 += RJ) {
+      if (!sync()) return;  // the buffer's last readers are through
+      if (r0 == 0) {
+        if (lane == 0) bar->bad[warp] = bad;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if ((lane & 3) == 0) bar->ml[warp][gr + 8 * x] = make_float2(m[x], l[x]);
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         if ((unsigned)(gr + 8 * x - r0) < RJ) {
@@ -310,7 +342,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
           for (int e = 0; e < N; ++e) acc[e] *= inv;
-          if (*(volatile int *)&bar->bad)
+          if (any_bad())
             add_wild<T, N>(a, g.s, g.h, Seq{g.start, g.count}, rr / a.G, D, col, acc);
           write_row<T, N>(a, g.s, g.h, rr, D, col, acc);
           if (col == 0) write_lse(a, g.s, g.h, rr, top, sum);
@@ -320,10 +352,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
           for (int e = 0; e < N; ++e) dst[e] = acc[e];
           if (col == 0) a.part_ml[(size_t)slot * ROWS + r] = make_float2(top, sum);
-          if (tid == 0 && r0 == 0) a.part_bad[slot] = *(volatile int *)&bar->bad;
+          if (tid == 0 && r0 == 0) a.part_bad[slot] = any_bad();
         }
       }
-      if (!sync()) return;  // the join buffer (behind the last rows, Q too) is free again
     }
   }
 }
@@ -473,7 +504,8 @@ pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
   CUtensorMap mk, mv;
   const uint64_t all = (uint64_t)c.pages * c.hkv * c.page;
   const int keys = rows == 16 ? kKeys : 128, box = c.page < keys ? c.page : keys;
-  if (!make_tile_map(&mk, k_pages, all, c.d, box) || !make_tile_map(&mv, v_pages, all, c.d, box))
+  auto make = rows == 16 ? make_tile_map_halves : make_tile_map;
+  if (!make(&mk, k_pages, all, c.d, box) || !make(&mv, v_pages, all, c.d, box))
     return PBS_ERR_CUDA;
   cudaStream_t cs = (cudaStream_t)st;
   const int grid = sm_count_cached();
