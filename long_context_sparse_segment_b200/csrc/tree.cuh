@@ -331,23 +331,26 @@ __device__ __forceinline__ void join(Part &p, const Part &q) {
 template <typename T, int D, int ROWS, int KEYS, int RB>
 __global__ void __launch_bounds__(kCombineThreads)
     tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
-  constexpr int C4 = D / 4, PG = kCombineThreads / (RB * C4);
-  static_assert(PG * RB * C4 == kCombineThreads, "threads");
+  constexpr int C4 = D / 4, E = RB * C4;  // results of a block, 4 columns each
+  constexpr int PG = E < kCombineThreads ? kCombineThreads / E : 1;
+  constexpr int VPT = E < kCombineThreads ? 1 : E / kCombineThreads;
+  static_assert(PG * E == VPT * kCombineThreads, "threads");
   __shared__ int sh[2 * kCombineThreads / 32];
-  __shared__ float4 so[kCombineThreads];
+  __shared__ float4 so[VPT * kCombineThreads];
   __shared__ float2 sml[PG][RB];
   const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = blockIdx.x * RB;  // first row of the (sequence, KV head)
   const Seq q = seq_of(a, s);
   const int rows = q.count * a.G;
-  // rows of the results: thread -> (row, 4 columns), neighbours along the row
-  const int wr = r0 + tid / C4, wc = tid % C4 * 4;
-  const bool writes = tid < RB * C4;
-  if (a.zero_rest && writes && wr >= rows && wr < a.tree * a.G) {
-    const float o[4] = {};
-    write_row<T, 4>(a, s, h, wr, D, wc, o);
-    if (wc == 0 && a.lse)
-      a.lse[((size_t)s * a.hq + h * a.G + wr % a.G) * a.tree + wr / a.G] = 0.f;
+  if (a.zero_rest && r0 + RB > rows) {
+    for (int e = tid; e < E; e += kCombineThreads) {
+      const int r = r0 + e / C4;
+      if (r < rows || r >= a.tree * a.G) continue;
+      const float o[4] = {};
+      write_row<T, 4>(a, s, h, r, D, e % C4 * 4, o);
+      if (e % C4 == 0 && a.lse)
+        a.lse[((size_t)s * a.hq + h * a.G + r % a.G) * a.tree + r / a.G] = 0.f;
+    }
   }
   if (r0 >= rows) {
     wait_previous();
@@ -375,54 +378,63 @@ __global__ void __launch_bounds__(kCombineThreads)
   const int slot0 = 2 * c0 + (run.start(c0) != u0);
   wait_previous();  // on every path, so that this kernel never ends before the other
   if (c0 == c1) return;
-  const int r = tid % RB, c4 = tid / RB % C4, pg = tid / (RB * C4);
-  const bool live = r0 + r < rows;
-  Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const int r = tid % RB, c4 = tid / RB % (C4 / VPT), pg = PG > 1 ? tid / E : 0;
+  Part p[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) p[v] = Part{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   int bad = 0;
-  if (live) {
+  if (r0 + r < rows) {
     const int rr = r0 % ROWS + r;
 #pragma unroll 4
     for (int c = c0 + pg; c <= c1; c += PG) {
       const size_t slot = c == c0 ? slot0 : 2 * c;
       const float2 ml = a.part_ml[slot * ROWS + rr];
-      join(p, Part{ml.x, ml.y, a.part_o[(slot * C4 + c4) * ROWS + rr]});
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+        join(p[v], Part{ml.x, ml.y, a.part_o[(slot * C4 + c4 + v * (C4 / VPT)) * ROWS + rr]});
       bad |= a.part_bad[slot];
     }
   }
   if (PG > 1) {
-    so[tid] = p.o;
-    if (c4 == 0) sml[pg][r] = make_float2(p.m, p.l);
-    bad = __syncthreads_or(bad);
+    so[tid] = p[0].o;
+    if (c4 == 0) sml[pg][r] = make_float2(p[0].m, p[0].l);
+  }
+  bad = __syncthreads_or(bad);
+  if (PG > 1) {
     if (pg == 0) {
 #pragma unroll
       for (int g = 1; g < PG; ++g)
-        join(p, Part{sml[g][r].x, sml[g][r].y, so[tid + g * RB * C4]});
+        join(p[0], Part{sml[g][r].x, sml[g][r].y, so[tid + g * E]});
     }
     __syncthreads();
-  } else {
-    bad = __syncthreads_or(bad);
   }
   if (pg == 0) {
-    so[r * C4 + c4] = p.o;
-    if (c4 == 0) sml[0][r] = make_float2(p.m, p.l);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) so[r * C4 + c4 + v * (C4 / VPT)] = p[v].o;
+    if (c4 == 0) sml[0][r] = make_float2(p[0].m, p[0].l);
   }
   __syncthreads();
-  if (!writes || wr >= rows) return;
-  const float2 ml = sml[0][tid / C4];
-  const float4 v = so[tid];
-  const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
-  float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-  if (bad) add_wild<T, 4>(a, s, h, q, wr / a.G, D, wc, o);
-  write_row<T, 4>(a, s, h, wr, D, wc, o);
-  if (wc == 0) write_lse(a, s, h, wr, ml.x, ml.y);
+  // neighbouring threads along a row
+  for (int e = tid; e < E; e += kCombineThreads) {
+    const int wr = r0 + e / C4, wc = e % C4 * 4;
+    if (wr >= rows) break;
+    const float2 ml = sml[0][e / C4];
+    const float4 v = so[e];
+    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+    float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+    if (bad) add_wild<T, 4>(a, s, h, q, wr / a.G, D, wc, o);
+    write_row<T, 4>(a, s, h, wr, D, wc, o);
+    if (wc == 0) write_lse(a, s, h, wr, ml.x, ml.y);
+  }
 }
 
 template <typename T, int D, int ROWS, int KEYS>
 cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
-  // 4 rows a block, and 16 where that makes more blocks than fit the GPU at
-  // once (four an SM)
+  // 4 rows a block, and 32 (16 where a row tile has no more) where that makes
+  // more blocks than fit the GPU at once (four an SM)
+  constexpr int MANY = ROWS < 32 ? 16 : 32;
   const int64_t rows = (int64_t)a.G * a.tree, few = ceil_div(rows, 4) * a.hkv * a.seqs;
-  const int rb = few <= 4 * 148 ? 4 : 16;
+  const int rb = few <= 4 * 148 ? 4 : MANY;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ceil_div(rows, rb), a.hkv, a.seqs);
   cfg.blockDim = dim3(kCombineThreads);
@@ -434,7 +446,7 @@ cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
   cfg.numAttrs = 1;
   return rb == 4
              ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, KEYS, 4>, a, grid)
-             : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, KEYS, 16>, a, grid);
+             : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, KEYS, MANY>, a, grid);
 }
 
 }  // namespace tree

@@ -145,32 +145,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       // In the order in which the products take them: PAIR K0, V0 K1, V1 K2
       // ...; otherwise K0 K1, V0 K2, V1 K3, ... A tile is up to 8 boxes of
       // page rows x H halves of 64 columns, one lane each.
-      const int box = min(a.page, kTile), pieces = kTile / box;
+      // A tile's page numbers are read one tile early and serve K, then V.
+      const int box = min(a.page, kTile), shift = 31 - __clz(a.page);
       const int half = lane % H, piece = lane / H;
+      const bool mine = piece < kTile / box;
+      constexpr int AHEAD = PAIR ? 1 : 2;  // K tiles in front of their V
       int kseq = 0, vseq = 0;
       bool ok = true;
-      auto load = [&](bool is_v, int k) {
+      auto load = [&](bool is_v, int k, int y) {  // y: the row, or -1: none
         int &seq = is_v ? vseq : kseq;
         const int S = is_v ? VS : KS, st = seq % S, use = seq / S;
-        const int t = k * kTile + piece * box;
-        const bool mine = piece < pieces && t < g.start + g.count;
-        int y = 0;
-        if (mine) {
-          int page = __ldg(a.table + (size_t)g.s * a.width + t / a.page);
-          if (page < 0 || page >= a.pages) {
-            report(a.err, PBS_ERR_DEVICE_ASSERT);
-            page = 0;
-          }
-          y = (page * a.hkv + g.h) * a.page + t % a.page;
-        }
-        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        const int boxes = __popc(__ballot_sync(0xffffffffu, y >= 0));
         uint64_t *full = is_v ? &sh->v_full[st] : &sh->k_full[st];
         if (use > 0 && !mbar_wait_warp(is_v ? &sh->v_empty[st] : &sh->k_empty[st], (use - 1) & 1,
                                        abort, a.err, is_v ? 21 : 11))
           return false;
         if (lane == 0) mbar_expect_tx(full, boxes * box * 128);
         __syncwarp();
-        if (mine)
+        if (y >= 0)
           tma_load_2d((is_v ? sV : sK) + (size_t)st * C::TILE + half * C::HALF + piece * box * 128,
                       is_v ? &tmV : &tmK, full, half * 64, y);
         __syncwarp();
@@ -178,12 +170,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       if (lane == 0) prefetch_map(&tmK), prefetch_map(&tmV);
-      constexpr int AHEAD = PAIR ? 1 : 2;
       while (ok && walk.next(a, &g)) {
-        for (int k = g.k0; k < min(g.k0 + AHEAD, g.k1) && ok; ++k) ok = load(false, k);
+        const int len = g.start + g.count;
+        const int32_t *row = a.table + (size_t)g.s * a.width;
+        auto page_of = [&](int k) {
+          const int t = k * kTile + piece * box;
+          return mine && k < g.k1 && t < len ? __ldg(row + (t >> shift)) : -1;
+        };
+        auto row_of = [&](int k, int page) {
+          const int t = k * kTile + piece * box;
+          if (!mine || k >= g.k1 || t >= len) return -1;
+          if (page < 0 || page >= a.pages) {
+            report(a.err, PBS_ERR_DEVICE_ASSERT);
+            page = 0;
+          }
+          return (page * a.hkv + g.h) * a.page + (t & (a.page - 1));
+        };
+        int y[AHEAD + 1];  // rows of tiles k .. k + AHEAD
+        int page = page_of(g.k0);
+        for (int k = g.k0; k < g.k0 + AHEAD && ok; ++k) {
+          const int ahead = page_of(k + 1);
+          y[k - g.k0] = row_of(k, page);
+          if (k < g.k1) ok = load(false, k, y[k - g.k0]);
+          page = ahead;
+        }
         for (int k = g.k0; k < g.k1 && ok; ++k) {
-          ok = load(true, k);
-          if (ok && k + AHEAD < g.k1) ok = load(false, k + AHEAD);
+          const int ahead = page_of(k + AHEAD + 1);
+          y[AHEAD] = row_of(k + AHEAD, page);
+          ok = load(true, k, y[0]);
+          if (ok && k + AHEAD < g.k1) ok = load(false, k + AHEAD, y[AHEAD]);
+#pragma unroll
+          for (int e = 0; e < AHEAD; ++e) y[e] = y[e + 1];
+          page = ahead;
         }
       }
       // every copy started here lands before the CTA exits
@@ -362,36 +380,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     seg_phase ^= 1;
     return ok;
   };
+  // A thread's 16-byte words of Q: LOADS rows, STEP apart, HELD of them in flight
+  // (one after the other: 12 us for 256 rows). The first are read before the wait
+  // for Q's place; before the end of the segment in front their registers cost
+  // more than they save (5 % on short contexts).
+  constexpr int CPR = D / 8, STEP = 256 / CPR, LOADS = ROWS / STEP, HELD = LOADS < 8 ? LOADS : 8;
+  const int ch = (tid - 128) % CPR, rq = (tid - 128) / CPR;
+  uint4 qv[HELD];
+  auto read_q = [&](const Segment &g, int first) {
+    const int rows = min(ROWS, g.count * a.G - g.rt * ROWS);
+#pragma unroll
+    for (int e = 0; e < HELD; ++e) {
+      const int r = rq + (first + e) * STEP;
+      qv[e] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int rr = g.rt * ROWS + r, i = rr / a.G, hd = g.h * a.G + rr - i * a.G;
+        qv[e] = *reinterpret_cast<const uint4 *>((const T *)a.q.p + (int64_t)g.s * a.q.batch +
+                                                 hd * a.q.head + i * a.q.row + ch * 8);
+      }
+    }
+  };
   bool ok = true;
   for (int seg = 0; ok && walk.next(a, &g); ++seg) {
+    read_q(g, 0);
     const int rows = min(ROWS, g.count * a.G - g.rt * ROWS);
     const int n = g.k1 - g.k0;
-    // Q: free once everybody is through with the segment before
+    // Q's place is free once everybody is through with the segment before
     ok = seg_sync();
     if (!ok) break;
-    {
-      constexpr int CPR = D / 8, STEP = 256 / CPR, LOADS = ROWS / STEP,
-                    BATCH = LOADS < 8 ? LOADS : 8;
-      const int ch = (tid - 128) % CPR, rq = (tid - 128) / CPR;
 #pragma unroll 1
-      for (int e0 = 0; e0 < LOADS; e0 += BATCH) {
-        uint4 v[BATCH];
+    for (int first = 0; first < LOADS; first += HELD) {
+      if (first > 0) read_q(g, first);
 #pragma unroll
-        for (int e = 0; e < BATCH; ++e) {
-          const int r = rq + (e0 + e) * STEP;
-          v[e] = make_uint4(0, 0, 0, 0);
-          if (r < rows) {
-            const int rr = g.rt * ROWS + r, i = rr / a.G, hd = g.h * a.G + rr - i * a.G;
-            v[e] = *reinterpret_cast<const uint4 *>((const T *)a.q.p + (int64_t)g.s * a.q.batch +
-                                                    hd * a.q.head + i * a.q.row + ch * 8);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < BATCH; ++e) {
-          const int r = rq + (e0 + e) * STEP;
-          *reinterpret_cast<uint4 *>(sQ + (r / kTile) * C::TILE + (ch >> 3) * C::HALF +
-                                     (r % kTile) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[e];
-        }
+      for (int e = 0; e < HELD; ++e) {
+        const int r = rq + (first + e) * STEP;
+        *reinterpret_cast<uint4 *>(sQ + (r / kTile) * C::TILE + (ch >> 3) * C::HALF +
+                                   (r % kTile) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = qv[e];
       }
     }
     fence_proxy_async_smem();
