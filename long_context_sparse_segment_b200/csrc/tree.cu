@@ -413,8 +413,9 @@ bool tree_supported(int hq, int tree, const pbs_cache &c) {
     return false;
   const int64_t rows = (int64_t)(hq / c.hkv) * tree;
   // units of a call, at most (the smallest tiles)
-  return rows < (1 << 22) && (double)c.seqs * c.hkv * ceil_div(rows, 16) *
-                                     ceil_div((int64_t)c.width * c.page, kKeys) < 2e9;
+  return rows < (1 << 22) &&
+         (double)c.seqs * c.hkv * ceil_div(rows, 16) *
+                 (ceil_div((int64_t)c.width * c.page, kKeys) + kExtra<256>) < 2e9;
 }
 
 int row_tile(int hq, int tree, const pbs_cache &c) {
