@@ -213,37 +213,41 @@ def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=No
 def _pools(k_pages, v_pages, table=None):
     """The pools [layers, pages, hkv, page, d] (or one layer's, 4-D)."""
     _on(k_pages, "k_pages")
-    _on(v_pages, "v_pages", k_pages.device)
-    if k_pages.dim() not in (4, 5) or k_pages.element_size() != 2:
+    dev, size = k_pages.device, k_pages.shape
+    _on(v_pages, "v_pages", dev)
+    if len(size) not in (4, 5) or k_pages.element_size() != 2:
         raise ValueError("k_pages must be [layers, pages, hkv, page, d] (or 4-D) of a 16-bit type")
-    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+    if v_pages.shape != size or v_pages.dtype is not k_pages.dtype:
         raise ValueError("v_pages must have the shape and type of k_pages")
-    if not k_pages.is_contiguous() or not v_pages.is_contiguous():
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages and v_pages must be contiguous")
-    if k_pages.numel() == 0:
+    if 0 in size:
         raise ValueError("k_pages is empty")
-    if k_pages.shape[-1] % 8:
+    if size[-1] % 8:
         raise ValueError("the head dimension must be a multiple of 8")
-    shape = k_pages.shape if k_pages.dim() == 5 else (1, *k_pages.shape)
-    seqs, width = (0, 1) if table is None else _table(table, k_pages.device)
-    return Cache(*shape, seqs, width)
+    seqs, width = (0, 1) if table is None else _table(table, dev)
+    return Cache(*(size if len(size) == 5 else (1, *size)), seqs, width)
 
 
 def _table(table, device=None):
     _on(table, "table", device)
-    if table.dim() != 2 or table.shape[1] < 1:
+    size = table.shape
+    if len(size) != 2 or size[1] < 1:
         raise ValueError("table must be [seqs, width]")
-    _ints(table, "table", table.shape, device)
-    return table.shape
+    _ints(table, "table", size, table.device)
+    return size
 
 
 def _books(table, refs, lens, page):
     seqs, width = _table(table)
-    _ints(refs, "refs", (refs.numel(),), table.device)
-    _ints(lens, "lens", (seqs,), table.device)
-    if refs.numel() < 1 or page < 1:
+    dev = table.device
+    _on(refs, "refs", dev)
+    pages = refs.numel()
+    _ints(refs, "refs", (pages,), dev)
+    _ints(lens, "lens", (seqs,), dev)
+    if pages < 1 or page < 1:
         raise ValueError("refs and page must not be empty")
-    return Cache(1, refs.numel(), 1, page, 8, seqs, width)
+    return Cache(1, pages, 1, page, 8, seqs, width)
 
 
 def _ws(op, c, n, device):
@@ -383,44 +387,49 @@ def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.
     asked; rows i >= count[s] are left as they were in ``out`` and are zero
     in what this call allocates (their lse too)."""
     c = _pools(k_pages, v_pages, table)
-    dev = k_pages.device
+    dev, t, size = k_pages.device, k_pages.dtype, getattr(q, "shape", None)
     _on(q, "q", dev)
     if k_pages.dim() != 4:
         raise ValueError("k_pages must be one layer's: [pages, hkv, page, d]")
-    if q.dtype not in _HALVES or q.dtype != k_pages.dtype:
+    if t not in _HALVES or q.dtype is not t:
         raise TypeError("q must be bf16 or fp16 and have the type of k_pages")
-    if q.dim() != 4 or q.shape[0] != c.seqs or q.shape[3] != c.d:
-        raise ValueError(f"q must be [{c.seqs}, hq, tree, {c.d}]")
-    _, hq, tree, d = q.shape
+    seqs = c.seqs
+    if len(size) != 4 or size[0] != seqs or size[3] != c.d:
+        raise ValueError(f"q must be [{seqs}, hq, tree, {c.d}]")
+    hq, tree = size[1], size[2]
     if hq < 1 or hq % c.hkv:
         raise ValueError("hq must be a multiple of hkv")
-    _ints(start, "start", (c.seqs,), dev)
+    _ints(start, "start", (seqs,), dev)
     if count is not None:
-        _ints(count, "count", (c.seqs,), dev)
+        _ints(count, "count", (seqs,), dev)
     if mask is not None:
-        _ints(mask, "mask", (c.seqs, tree, (tree + 31) // 32), dev)
+        _ints(mask, "mask", (seqs, tree, (tree + 31) // 32), dev)
     zero = count is not None and out is None
     if out is None:
         out = _fresh(q)
     else:
         _on(out, "out", dev)
-        if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        if out.shape != size or out.dtype is not t or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape and type")
         if out.data_ptr() == q.data_ptr() and out.numel():
             raise ValueError("out must not be q")
-    if not lse:
-        l = None
-    elif zero or count is None:
-        l = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+    l = None
+    if lse:
+        l = out.new_empty(size[:3], dtype=torch.float32)
+        if count is not None and not zero:
+            l.zero_()
+    if not (seqs and tree):
+        return (out, l) if lse else out
+    need = lib().pbs_tree_workspace_bytes(hq, tree, c)
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
-        l = torch.zeros(q.shape[:3], dtype=torch.float32, device=dev)
-    need = lib().pbs_tree_workspace_bytes(hq, tree, c) if q.numel() else 0
-    if ws is None or ws.numel() * ws.element_size() < need:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    rows = _rows(q, "q") if q.numel() else _NONE
-    _call("pbs_tree_attn", dev, rows, _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(start),
-          _ptr(count), _ptr(mask), _ptr(out), _ptr(l), hq, tree, c, scale, int(zero),
-          _TYPES[q.dtype], _ptr(ws), need)
+        _on(ws, "ws", dev)
+        if not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+            raise ValueError(f"ws must be contiguous, of {need} bytes at least")
+    _call("pbs_tree_attn", dev, _rows(q, "q"), k_pages.data_ptr(), v_pages.data_ptr(),
+          table.data_ptr(), start.data_ptr(), _ptr(count), _ptr(mask), out.data_ptr(), _ptr(l),
+          hq, tree, c, scale, zero, _TYPES[t], ws.data_ptr(), need)
     return (out, l) if lse else out
 
 
