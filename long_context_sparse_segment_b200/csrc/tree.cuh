@@ -344,11 +344,10 @@ template <typename T, int D, int ROWS, int KEYS, int RB>
 __global__ void __launch_bounds__(kCombineThreads)
     tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
   constexpr int C4 = D / 4, E = RB * C4;  // results of a block, 4 columns each
-  constexpr int PG = E < kCombineThreads ? kCombineThreads / E : 1;
-  constexpr int VPT = E < kCombineThreads ? 1 : E / kCombineThreads;
-  static_assert(PG * E == VPT * kCombineThreads, "threads");
+  constexpr int PG = kCombineThreads / E;
+  static_assert(PG * E == kCombineThreads, "threads");
   __shared__ int sh[2 * kCombineThreads / 32];
-  __shared__ float4 so[VPT * kCombineThreads];
+  __shared__ float4 so[kCombineThreads];
   __shared__ float2 sml[PG][RB];
   const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = blockIdx.x * RB;  // first row of the (sequence, KV head)
@@ -390,10 +389,8 @@ __global__ void __launch_bounds__(kCombineThreads)
   const int slot0 = 2 * c0 + (run.start(c0) < u0);
   wait_previous();  // on every path, so that this kernel never ends before the other
   if (c0 == c1) return;
-  const int r = tid % RB, c4 = tid / RB % (C4 / VPT), pg = PG > 1 ? tid / E : 0;
-  Part p[VPT];
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) p[v] = Part{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const int r = tid % RB, c4 = tid / RB % C4, pg = tid / E;
+  Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   int bad = 0;
   if (r0 + r < rows) {
     const int rr = r0 % ROWS + r;
@@ -401,29 +398,26 @@ __global__ void __launch_bounds__(kCombineThreads)
     for (int c = c0 + pg; c <= c1; c += PG) {
       const size_t slot = c == c0 ? slot0 : 2 * c;
       const float2 ml = a.part_ml[slot * ROWS + rr];
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-        join(p[v], Part{ml.x, ml.y, a.part_o[(slot * C4 + c4 + v * (C4 / VPT)) * ROWS + rr]});
+      join(p, Part{ml.x, ml.y, a.part_o[(slot * C4 + c4) * ROWS + rr]});
       bad |= a.part_bad[slot];
     }
   }
   if (PG > 1) {
-    so[tid] = p[0].o;
-    if (c4 == 0) sml[pg][r] = make_float2(p[0].m, p[0].l);
+    so[tid] = p.o;
+    if (c4 == 0) sml[pg][r] = make_float2(p.m, p.l);
   }
   bad = __syncthreads_or(bad);
   if (PG > 1) {
     if (pg == 0) {
 #pragma unroll
       for (int g = 1; g < PG; ++g)
-        join(p[0], Part{sml[g][r].x, sml[g][r].y, so[tid + g * E]});
+        join(p, Part{sml[g][r].x, sml[g][r].y, so[tid + g * E]});
     }
     __syncthreads();
   }
   if (pg == 0) {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) so[r * C4 + c4 + v * (C4 / VPT)] = p[v].o;
-    if (c4 == 0) sml[0][r] = make_float2(p[0].m, p[0].l);
+    so[r * C4 + c4] = p.o;
+    if (c4 == 0) sml[0][r] = make_float2(p.m, p.l);
   }
   __syncthreads();
   // neighbouring threads along a row
@@ -442,11 +436,11 @@ __global__ void __launch_bounds__(kCombineThreads)
 
 template <typename T, int D, int ROWS, int KEYS>
 cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
-  // 4 rows a block, and 32 (16 where a row tile has no more) where that makes
-  // more blocks than fit the GPU at once (four an SM)
-  constexpr int MANY = ROWS < 32 ? 16 : 32;
+  // 4 rows a block, and 16 where that makes more blocks than fit the GPU at once
+  // (four an SM): 4 rows with 4 threads a part are 2.5 us quicker on one sequence
+  // over 8192 tokens, 16 rows 12 us on 64 drafts of 8 sequences
   const int64_t rows = (int64_t)a.G * a.tree, few = ceil_div(rows, 4) * a.hkv * a.seqs;
-  const int rb = few <= 4 * 148 ? 4 : MANY;
+  const int rb = few <= 4 * 148 ? 4 : 16;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ceil_div(rows, rb), a.hkv, a.seqs);
   cfg.blockDim = dim3(kCombineThreads);
@@ -458,7 +452,7 @@ cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
   cfg.numAttrs = 1;
   return rb == 4
              ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, KEYS, 4>, a, grid)
-             : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, KEYS, MANY>, a, grid);
+             : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, KEYS, 16>, a, grid);
 }
 
 }  // namespace tree
