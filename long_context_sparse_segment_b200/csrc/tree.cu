@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
     }
     const int slot = 2 * blockIdx.x + (seg > 0);
+    if (tid == 0) tell_item(a, g, place.run, slot);
     constexpr int RJ = C::RJ, N = D * RJ / (32 * kConsumers);  // columns a thread joins
     auto any_bad = [&]() {
       int x = 0;
@@ -424,14 +425,17 @@ int row_tile(int hq, int tree, const pbs_cache &c) {
 }
 
 struct Parts {
-  size_t o, ml, bad, bytes;
+  size_t o, ml, items, bad, bytes;
+  int tiles;
 };
-Parts parts(int rows, int d) {
+Parts parts(int rows, int hq, int tree, const pbs_cache &c) {
   const size_t slots = 2 * (size_t)sm_count_cached();
   Parts p;
+  p.tiles = (int)ceil_div((int64_t)(hq / c.hkv) * tree, rows);
   p.o = 0;
-  p.ml = slots * rows * d * 4;
-  p.bad = p.ml + slots * rows * 8;
+  p.ml = slots * rows * c.d * 4;
+  p.items = p.ml + slots * rows * 8;
+  p.bad = p.items + (size_t)c.seqs * c.hkv * p.tiles * 8;
   p.bytes = p.bad + slots * 4;
   return p;
 }
@@ -444,7 +448,7 @@ cudaError_t run_mma(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs
   const cudaError_t e = allow_smem<kern>((int)C::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<grid, kMmaThreads, C::SMEM, st>>>(mk, mv, a);
-  return launch_combine<T, D, C::ROWS, kKeys>(a, grid, st);
+  return launch_combine<T, D, C::ROWS>(a, grid, st);
 }
 
 }  // namespace
@@ -470,7 +474,7 @@ pbs_status pbs_tree_mask(const int32_t *parents, uint32_t *mask, int32_t *depth,
 size_t pbs_tree_workspace_bytes(int hq, int tree, pbs_cache c) {
   if (!tree_shape_ok(hq, tree, c) || !tree_supported(hq, tree, c) || c.seqs == 0 || tree == 0)
     return 0;
-  return parts(row_tile(hq, tree, c), c.d).bytes;
+  return parts(row_tile(hq, tree, c), hq, tree, c).bytes;
 }
 
 pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
@@ -488,7 +492,7 @@ pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
       !aligned16(out) || ((uintptr_t)lse & 3u) || !ws || !aligned16(ws))
     return PBS_ERR_INVALID_ARG;
   const int rows = row_tile(hq, tree, c);
-  const Parts p = parts(rows, c.d);
+  const Parts p = parts(rows, hq, tree, c);
   if (ws_bytes < p.bytes) return PBS_ERR_WORKSPACE;
   TreeArgs a{};
   a.q = q, a.table = table, a.start = start, a.count = count, a.mask = mask, a.v_pages = v_pages;
@@ -496,6 +500,8 @@ pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
   a.part_o = (float4 *)((uint8_t *)ws + p.o);
   a.part_ml = (float2 *)((uint8_t *)ws + p.ml);
   a.part_bad = (int *)((uint8_t *)ws + p.bad);
+  a.items = (int2 *)((uint8_t *)ws + p.items);
+  a.tiles = p.tiles;
   a.err = error_word();
   a.hq = hq, a.hkv = c.hkv, a.G = hq / c.hkv, a.tree = tree, a.words = (tree + 31) / 32;
   a.seqs = c.seqs, a.width = c.width, a.page = c.page, a.pages = c.pages;

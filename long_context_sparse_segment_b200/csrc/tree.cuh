@@ -35,8 +35,10 @@ struct TreeArgs {
   float4 *part_o;   // [2 grid][d / 4][rows]: neighbouring rows side by side
   float2 *part_ml;  // [2 grid][rows]: running maximum (log2) and sum
   int *part_bad;    // [2 grid]: drafted V rows with NaN or infinity met
+  int2 *items;      // [seqs][hkv][tiles]: an item's first part, and its last CTA
   int *err;
   int hq, hkv, G, tree, words, seqs, width, page, pages;
+  int tiles;  // row tiles of `tree` drafts
   int zero_rest;  // rows behind a sequence's count become 0 instead of staying
   float sl2;
 };
@@ -79,6 +81,7 @@ __device__ __forceinline__ int units_of(const TreeArgs &a, const Seq &q) {
 // that unit u belongs to.
 struct Runs {
   int base, extra;
+  Runs() = default;
   __device__ __forceinline__ Runs(int total, int runs)
       : base(total / runs), extra(total - total / runs * runs) {}
   __device__ __forceinline__ int start(int c) const { return c * base + min(c, extra); }
@@ -92,6 +95,7 @@ struct Runs {
 // first lies in with the units before that one.
 struct Place {
   int u0, u1, s, before;
+  Runs run;
 };
 
 // Every thread of the block (NT of them, a multiple of 32) calls it; false
@@ -118,7 +122,7 @@ __device__ __forceinline__ bool find_place(const TreeArgs &a, int *sum, Place *p
   const int runs = min(total, (int)gridDim.x);
   if ((int)blockIdx.x >= runs) return false;
   const Runs run(total, runs);
-  p->u0 = run.start(blockIdx.x), p->u1 = run.start(blockIdx.x + 1);
+  p->u0 = run.start(blockIdx.x), p->u1 = run.start(blockIdx.x + 1), p->run = run;
   int base = 0;
   for (int s0 = 0;; s0 += 32) {
     if (s0 > 0) x = units(s0 + lane);
@@ -145,7 +149,17 @@ struct Segment {
   int start, count;  // tokens, drafts
   int k0, k1;        // key tiles
   int whole;         // all of the item's key tiles
+  int last;          // the item's last unit
 };
+
+// Where an item's parts are, told by the CTA that has its first tile: the slot
+// of that part, and the CTA that has its last tile (the same one: no parts).
+__device__ __forceinline__ void tell_item(const TreeArgs &a, const Segment &g, const Runs &run,
+                                          int slot) {
+  if (g.k0 == 0)
+    a.items[((size_t)g.s * a.hkv + g.h) * a.tiles + g.rt] =
+        make_int2(slot, g.whole ? (int)blockIdx.x : run.owner(g.last));
+}
 
 // The segments of a run, one after the other.
 template <int ROWS, int KEYS>
@@ -168,6 +182,7 @@ struct Walk {
       g->k0 = max(at, 0);
       g->k1 = min(kt, at + u1 - u);
       g->whole = g->k1 - g->k0 == kt;
+      g->last = u - at + kt - 1;
       u += min(kt - at, u1 - u);
       if (g->k1 > g->k0) return true;  // else the run ends before the item's first tile
     }
@@ -311,12 +326,13 @@ __device__ __forceinline__ float part_scale(float m, float top) {
 }
 
 // -------------------------------------------------------------------- combine
-// Joins the parts of the rows that several CTAs worked on. A block takes RB
-// rows of one (sequence, KV head): a thread holds 4 columns of a row and every
-// PG-th part of it, in order; the PG partial results are joined in shared
-// memory. It is launched while the attention kernel still runs (programmatic
-// dependent launch): what comes before the wait reads only the call's inputs.
-// Bound by latency: a part is read once, all of a thread's reads in flight.
+// Joins the parts of the rows that several CTAs worked on. A block takes every
+// gridDim.x-th group of RB rows of one (sequence, KV head): a thread holds 4
+// columns of a row and every PG-th part of it, in order; the PG partial results
+// are joined in shared memory. It is launched while the attention kernel still
+// runs (programmatic dependent launch). Bound by latency: a part is read once,
+// a thread's reads in flight together; most blocks find that nobody shared
+// their items and end.
 constexpr int kCombineThreads = 512;
 
 // Allows the kernel launched behind this one to start.
@@ -340,109 +356,91 @@ __device__ __forceinline__ void join(Part &p, const Part &q) {
   p.o.z = p.o.z * f + q.o.z * g, p.o.w = p.o.w * f + q.o.w * g;
 }
 
-template <typename T, int D, int ROWS, int KEYS, int RB>
+template <typename T, int D, int ROWS, int RB>
 __global__ void __launch_bounds__(kCombineThreads)
     tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
-  constexpr int C4 = D / 4, E = RB * C4;  // results of a block, 4 columns each
+  constexpr int C4 = D / 4, E = RB * C4;  // results of a group, 4 columns each
   constexpr int PG = kCombineThreads / E;
-  static_assert(PG * E == kCombineThreads, "threads");
-  __shared__ int sh[2 * kCombineThreads / 32];
+  static_assert(PG * E == kCombineThreads && ROWS % RB == 0, "threads");
   __shared__ float4 so[kCombineThreads];
   __shared__ float2 sml[PG][RB];
-  const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r0 = blockIdx.x * RB;  // first row of the (sequence, KV head)
+  const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
   const Seq q = seq_of(a, s);
-  const int rows = q.count * a.G;
-  if (a.zero_rest && r0 + RB > rows) {
-    for (int e = tid; e < E; e += kCombineThreads) {
-      const int r = r0 + e / C4;
-      if (r < rows || r >= a.tree * a.G) continue;
-      const float o[4] = {};
-      write_row<T, 4>(a, s, h, r, D, e % C4 * 4, o);
-      if (e % C4 == 0 && a.lse)
-        a.lse[((size_t)s * a.hq + h * a.G + r % a.G) * a.tree + r / a.G] = 0.f;
-    }
-  }
-  if (r0 >= rows) {
-    wait_previous();
-    return;
-  }
-  // units before this sequence, and all
-  int mine = 0, all = 0;
-  for (int i = tid; i < a.seqs; i += kCombineThreads) {
-    const int x = units_of<ROWS, KEYS>(a, seq_of(a, i));
-    all += x;
-    if (i < s) mine += x;
-  }
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  all = __reduce_add_sync(0xffffffffu, all);
-  constexpr int W = kCombineThreads / 32;
-  if (lane == 0) sh[warp] = mine, sh[W + warp] = all;
-  __syncthreads();
-  int u0 = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) u0 += sh[w], total += sh[W + w];
-  const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(rows, ROWS);
-  u0 += (h * rts + r0 / ROWS) * (kt + kExtra<ROWS>);
-  const Runs run(total, min(total, grid));
-  const int c0 = run.owner(u0 + kExtra<ROWS>), c1 = run.owner(u0 + kExtra<ROWS> + kt - 1);
-  const int slot0 = 2 * c0 + (run.start(c0) < u0);
-  wait_previous();  // on every path, so that this kernel never ends before the other
-  if (c0 == c1) return;
+  const int rows = q.count * a.G, all = a.tree * a.G;  // of the (sequence, KV head)
   const int r = tid % RB, c4 = tid / RB % C4, pg = tid / E;
-  Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  int bad = 0;
-  if (r0 + r < rows) {
-    const int rr = r0 % ROWS + r;
-#pragma unroll 4
-    for (int c = c0 + pg; c <= c1; c += PG) {
-      const size_t slot = c == c0 ? slot0 : 2 * c;
-      const float2 ml = a.part_ml[slot * ROWS + rr];
-      join(p, Part{ml.x, ml.y, a.part_o[(slot * C4 + c4) * ROWS + rr]});
-      bad |= a.part_bad[slot];
+  // results: neighbouring threads along a row
+  const int er = tid / C4, ec = tid % C4 * 4;
+  wait_previous();  // on every path, so that this kernel never ends before the other
+  for (int r0 = blockIdx.x * RB; r0 < all; r0 += gridDim.x * RB) {
+    if (a.zero_rest && tid < E && r0 + er >= rows && r0 + er < all) {
+      const float o[4] = {};
+      write_row<T, 4>(a, s, h, r0 + er, D, ec, o);
+      if (ec == 0 && a.lse)
+        a.lse[((size_t)s * a.hq + h * a.G + (r0 + er) % a.G) * a.tree + (r0 + er) / a.G] = 0.f;
     }
-  }
-  if (PG > 1) {
-    so[tid] = p.o;
-    if (c4 == 0) sml[pg][r] = make_float2(p.m, p.l);
-  }
-  bad = __syncthreads_or(bad);
-  if (PG > 1) {
-    if (pg == 0) {
+    if (r0 >= rows) continue;
+    const int2 item = a.items[((size_t)s * a.hkv + h) * a.tiles + r0 / ROWS];
+    const int slot0 = item.x, c0 = slot0 >> 1, c1 = item.y;
+    if (c0 == c1) continue;
+    if (c0 < 0 || c1 < c0 || c1 >= grid) {  // the attention kernel gave up before
+      if (tid == 0) report(a.err, PBS_ERR_DEVICE_ASSERT);
+      continue;
+    }
+    Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    int bad = 0;
+    if (r0 + r < rows) {
+      const int rr = r0 % ROWS + r;
+#pragma unroll 4
+      for (int c = c0 + pg; c <= c1; c += PG) {
+        const size_t slot = c == c0 ? slot0 : 2 * c;
+        const float2 ml = a.part_ml[slot * ROWS + rr];
+        join(p, Part{ml.x, ml.y, a.part_o[(slot * C4 + c4) * ROWS + rr]});
+        bad |= a.part_bad[slot];
+      }
+    }
+    if (PG > 1) {
+      so[tid] = p.o;
+      if (c4 == 0) sml[pg][r] = make_float2(p.m, p.l);
+    }
+    bad = __syncthreads_or(bad);
+    if (PG > 1) {
+      if (pg == 0) {
 #pragma unroll
-      for (int g = 1; g < PG; ++g)
-        join(p, Part{sml[g][r].x, sml[g][r].y, so[tid + g * E]});
+        for (int g = 1; g < PG; ++g)
+          join(p, Part{sml[g][r].x, sml[g][r].y, so[tid + g * E]});
+      }
+      __syncthreads();
+    }
+    if (pg == 0) {
+      so[r * C4 + c4] = p.o;
+      if (c4 == 0) sml[0][r] = make_float2(p.m, p.l);
+    }
+    __syncthreads();
+    if (tid < E && r0 + er < rows) {
+      const float2 ml = sml[0][er];
+      const float4 v = so[tid];
+      const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+      float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+      if (bad) add_wild<T, 4>(a, s, h, q, (r0 + er) / a.G, D, ec, o);
+      write_row<T, 4>(a, s, h, r0 + er, D, ec, o);
+      if (ec == 0) write_lse(a, s, h, r0 + er, ml.x, ml.y);
     }
     __syncthreads();
   }
-  if (pg == 0) {
-    so[r * C4 + c4] = p.o;
-    if (c4 == 0) sml[0][r] = make_float2(p.m, p.l);
-  }
-  __syncthreads();
-  // neighbouring threads along a row
-  for (int e = tid; e < E; e += kCombineThreads) {
-    const int wr = r0 + e / C4, wc = e % C4 * 4;
-    if (wr >= rows) break;
-    const float2 ml = sml[0][e / C4];
-    const float4 v = so[e];
-    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
-    float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-    if (bad) add_wild<T, 4>(a, s, h, q, wr / a.G, D, wc, o);
-    write_row<T, 4>(a, s, h, wr, D, wc, o);
-    if (wc == 0) write_lse(a, s, h, wr, ml.x, ml.y);
-  }
 }
 
-template <typename T, int D, int ROWS, int KEYS>
+template <typename T, int D, int ROWS>
 cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
-  // 4 rows a block, and 16 where that makes more blocks than fit the GPU at once
-  // (four an SM): 4 rows with 4 threads a part are 2.5 us quicker on one sequence
-  // over 8192 tokens, 16 rows 12 us on 64 drafts of 8 sequences
-  const int64_t rows = (int64_t)a.G * a.tree, few = ceil_div(rows, 4) * a.hkv * a.seqs;
-  const int rb = few <= 4 * 148 ? 4 : 16;
+  // 4 rows a group, and 16 where that makes more groups than fit the GPU at once
+  // (four blocks an SM): 4 rows, with 4 threads a part, are 3 us quicker on one
+  // sequence over 8192 tokens, 16 rows 14 us on 64 drafts of 8 sequences. Blocks
+  // for four such rounds, then they walk the groups.
+  const int64_t rows = (int64_t)a.G * a.tree, heads = (int64_t)a.hkv * a.seqs, fit = 4 * 148;
+  const int rb = ceil_div(rows, 4) * heads <= fit ? 4 : 16;
+  int64_t gx = ceil_div(rows, rb);
+  if (gx * heads > 4 * fit) gx = ceil_div(4 * fit, heads);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ceil_div(rows, rb), a.hkv, a.seqs);
+  cfg.gridDim = dim3((unsigned)gx, a.hkv, a.seqs);
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = st;
   cudaLaunchAttribute at{};
@@ -450,9 +448,8 @@ cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return rb == 4
-             ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, KEYS, 4>, a, grid)
-             : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, KEYS, 16>, a, grid);
+  return rb == 4 ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, 4>, a, grid)
+                 : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, 16>, a, grid);
 }
 
 }  // namespace tree

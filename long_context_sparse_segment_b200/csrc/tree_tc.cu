@@ -516,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) break;
     // ------------------------------------------------------- the item's end
     const int slot = 2 * blockIdx.x + (seg > 0);
+    if (tid == 128) tell_item(a, g, sh->place.run, slot);
     const int rr = g.rt * ROWS + row;
     float top = m_used, sum = l, f[2] = {1.f, 1.f};
     if (!PAIR) {
@@ -614,7 +615,7 @@ cudaError_t run(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a,
   }
   if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
   kern<<<grid, kThreads, C::SMEM, st>>>(mk, mv, a);
-  return launch_combine<T, D, C::ROWS, kTile>(a, grid, st);
+  return launch_combine<T, D, C::ROWS>(a, grid, st);
 }
 
 template <typename T>
