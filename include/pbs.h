@@ -558,14 +558,16 @@ pbs_status pbs_cache_compact(void *k_pages, void *v_pages, int32_t *table, int32
 /*
  * pbs_cache_accept - the accepted drafts of each sequence moved behind its
  * prefix: token start[s] + path[s][i] becomes token start[s] + i for i <
- * count[s] (all `tree` when count is NULL), in both pools and every layer.
- * path [seqs, tree] ascends strictly, 0 <= path < tree, so a draft only
- * moves down; a sequence whose path does not, is reported and left alone.
+ * count[s] (all n when count is NULL), in both pools and every layer. path
+ * [seqs, n] ascends strictly from 0 on, so a draft only moves down; a
+ * sequence whose path does not, or names a token that no page holds, is
+ * reported and left alone.
+ * The pages from token start[s] on must be the sequence's own (reserved).
  * lens (may be NULL): lens[s] = start[s] + count[s] where the path is good.
  */
 pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,
                             const int32_t *start, const int32_t *path, const int32_t *count,
-                            int32_t *lens, int tree, pbs_cache c, pbs_stream_t st);
+                            int32_t *lens, int n, pbs_cache c, pbs_stream_t st);
 
 /*
  * pbs_tree_mask - which drafts see which, from their parents. parents
@@ -596,7 +598,9 @@ pbs_status pbs_tree_mask(const int32_t *parents, uint32_t *mask, int32_t *depth,
  *        i >= count[s] are left as they were, or with zero_rest become 0,
  *        their lse too.
  * A token that a row does not see has no part in it, whatever its K and V
- * hold (NaN and infinities too).
+ * hold (NaN and infinities too). The workspace belongs to one call at a time:
+ * calls that may overlap on the GPU need one each. The lengths, tables and
+ * masks may not change while the call runs.
  */
 pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
                          const int32_t *table, const int32_t *start, const int32_t *count,
@@ -613,7 +617,8 @@ size_t pbs_tree_workspace_bytes(int hq, int tree, pbs_cache c);
  * (a pbs_status; PBS_OK when no kernel reported a problem) and clears it.
  * `detail` (nullable) receives a diagnostic: for PBS_ERR_TIMEOUT the place
  * of the wait that ran out (tens digit: 1 K' loader, 2 V' loader, 3 MMA
- * issuer, 4 softmax; units digit: which wait), else 0.
+ * issuer, 4 softmax, 5 the warps of pbs_tree_attn that join their results;
+ * units digit: which wait), else 0.
  */
 pbs_status pbs_get_device_status(pbs_stream_t st, int *code, int *detail);
 

@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kAcceptThreads)
     const int i = i0 + tid;
     if (i >= n) return true;
     const int x = __ldg(p + i), before = i > 0 ? __ldg(p + i - 1) : -1;
-    if (x < 0 || x >= tree || before >= x) return false;
+    if (x < 0 || before >= x) return false;
     const int64_t a = token_word(row, (int64_t)st + x, c, words);
     const int64_t b = token_word(row, (int64_t)st + i, c, words);
     from[tid] = a;
@@ -545,7 +545,7 @@ pbs_status pbs_cache_copy(void *k_pages, void *v_pages, const int32_t *src, cons
   if (need) {
     owner = (int32_t *)ws;
     if (cudaMemsetAsync(owner, 0xff, need, cs) != cudaSuccess) return PBS_ERR_CUDA;
-    owner_kernel<<<(n + 255) / 256, 256, 0, cs>>>(dst, n, c.pages, owner);
+    owner_kernel<<<n / 256 + 1, 256, 0, cs>>>(dst, n, c.pages, owner);
   }
   copy_kernel<<<copy_grid(c, n), kCopyThreads, 0, cs>>>((uint4 *)k_pages, (uint4 *)v_pages, src,
                                                        dst, n, nullptr, owner, c, page_words(c),

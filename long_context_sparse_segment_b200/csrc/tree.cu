@@ -12,6 +12,9 @@
 // keys, four warps a tile (16 keys each) and the two halves in turn, each
 // with its own maximum, sum and output, joined when the item ends; a ninth
 // warp brings the tiles by TMA, page by page, into a ring.
+#include <stdlib.h>
+#include <string.h>
+
 #include "internal.h"
 #include "tree_tc.h"
 
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
         if (lane == 0) mbar_expect_tx(&bar->full[st], boxes * box * D * 2);
         __syncwarp();
-        if (load)
+        if (load && !(a.fault && it == 0 && kv == 0))
           tma_load_3d(ring + (size_t)(2 * st + kv) * C::KV + piece * box * D * 2,
                       kv ? &tmV : &tmK, &bar->full[st], 0, y, 0);
         __syncwarp();
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     cp_async_wait_all();
     int never = 0;
     for (int i = it > ST ? it - ST : 0; i < it; ++i)
-      mbar_wait(&bar->full[i % ST], (i / ST) & 1, &never, nullptr);
+      if (!(a.fault && i == 0)) mbar_wait(&bar->full[i % ST], (i / ST) & 1, &never, nullptr);
     return;
   }
 
@@ -445,9 +448,11 @@ cudaError_t run_mma(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs
                     cudaStream_t st) {
   using C = MmaCfg<D>;
   constexpr auto kern = tree_mma_kernel<T, D>;
-  const cudaError_t e = allow_smem<kern>((int)C::SMEM);
+  cudaError_t e = allow_smem<kern>((int)C::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<grid, kMmaThreads, C::SMEM, st>>>(mk, mv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   return launch_combine<T, D, C::ROWS>(a, grid, st);
 }
 
@@ -508,6 +513,10 @@ pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
   const float sigma = scale > 0.f ? scale : (float)(1.0 / sqrt((double)c.d));
   a.sl2 = sigma * kLog2e;
   a.zero_rest = zero_rest != 0;
+  // PBS_FAULT_INJECT=tree makes every CTA leave its first K tile out, so that
+  // bounded waits run out (used by the failure-detection tests)
+  const char *fi = getenv("PBS_FAULT_INJECT");
+  a.fault = fi && strcmp(fi, "tree") == 0;
   CUtensorMap mk, mv;
   const uint64_t all = (uint64_t)c.pages * c.hkv * c.page;
   const int keys = rows == 16 ? kKeys : 128, box = c.page < keys ? c.page : keys;

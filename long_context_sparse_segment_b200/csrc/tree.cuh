@@ -39,6 +39,7 @@ struct TreeArgs {
   int *err;
   int hq, hkv, G, tree, words, seqs, width, page, pages;
   int tiles;  // row tiles of `tree` drafts
+  int fault;      // the first K tile of every CTA stays out (failure tests)
   int zero_rest;  // rows behind a sequence's count become 0 instead of staying
   float sl2;
 };
@@ -124,7 +125,7 @@ __device__ __forceinline__ bool find_place(const TreeArgs &a, int *sum, Place *p
   const Runs run(total, runs);
   p->u0 = run.start(blockIdx.x), p->u1 = run.start(blockIdx.x + 1), p->run = run;
   int base = 0;
-  for (int s0 = 0;; s0 += 32) {
+  for (int s0 = 0; s0 < a.seqs; s0 += 32) {
     if (s0 > 0) x = units(s0 + lane);
     int inc = x;
 #pragma unroll
@@ -141,6 +142,7 @@ __device__ __forceinline__ bool find_place(const TreeArgs &a, int *sum, Place *p
     }
     base = __shfl_sync(0xffffffffu, inc, 31);
   }
+  return false;  // only when somebody changes the lengths under this call
 }
 
 // A piece of a CTA's run inside one item.
@@ -172,7 +174,8 @@ struct Walk {
       Seq q = seq_of(a, s);
       for (int n; u >= before + (n = units_of<ROWS, KEYS>(a, q));) {
         before += n;
-        q = seq_of(a, ++s);
+        if (++s >= a.seqs) return false;  // the lengths changed under this call
+        q = seq_of(a, s);
       }
       constexpr int X = kExtra<ROWS>;
       const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(q.count * a.G, ROWS);

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return false;
         if (lane == 0) mbar_expect_tx(full, boxes * box * 128);
         __syncwarp();
-        if (y >= 0)
+        if (y >= 0 && !(a.fault && !is_v && seq == 0))
           tma_load_2d((is_v ? sV : sK) + (size_t)st * C::TILE + half * C::HALF + piece * box * 128,
                       is_v ? &tmV : &tmK, full, half * 64, y);
         __syncwarp();
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every copy started here lands before the CTA exits
       int never = 0;
       for (int i = kseq > KS ? kseq - KS : 0; i < kseq; ++i)
-        mbar_wait(&sh->k_full[i % KS], (i / KS) & 1, &never, nullptr);
+        if (!(a.fault && i == 0)) mbar_wait(&sh->k_full[i % KS], (i / KS) & 1, &never, nullptr);
       for (int i = vseq > VS ? vseq - VS : 0; i < vseq; ++i)
         mbar_wait(&sh->v_full[i % VS], (i / VS) & 1, &never, nullptr);
     } else if (warp == 1) {
@@ -615,6 +615,8 @@ cudaError_t run(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a,
   }
   if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
   kern<<<grid, kThreads, C::SMEM, st>>>(mk, mv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   return launch_combine<T, D, C::ROWS>(a, grid, st);
 }
 

@@ -118,20 +118,22 @@ def rope_freqs(rot, base=10000.0, scaling=None, device=None):
     """
     if rot < 0 or rot % 16:
         raise ValueError("rot must be a non-negative multiple of 16")
-    if not base > 0:
-        raise ValueError("base must be positive")
+    if not base > 1:
+        raise ValueError("base must be above 1")
     i = torch.arange(rot // 2, dtype=torch.float64)
     freq = lambda b: torch.pow(torch.tensor(float(b), dtype=torch.float64), -2.0 * i / max(rot, 1))
     f, gain = freq(base), 1.0
     if scaling is not None:
         s = dict(scaling)
-        kind, factor = s.pop("type"), float(s.pop("factor"))
+        kind, factor = s.pop("type", None), float(s.pop("factor", 0))
         if not factor >= 1:
             raise ValueError("factor must be at least 1")
         if kind == "linear":
             f = f / factor
         elif kind == "ntk":
             f = freq(base * factor ** (rot / max(rot - 2, 1)))
+        elif kind in ("ramp", "yarn") and not s.get("original", 0) > 0:
+            raise ValueError(f"{kind} needs original, the tokens trained on")
         elif kind == "ramp":
             original, low, high = s.pop("original"), s.pop("low", 1.0), s.pop("high", 4.0)
             if not high > low:
@@ -250,6 +252,14 @@ def _books(table, refs, lens, page):
     return Cache(1, pages, 1, page, 8, seqs, width)
 
 
+def _pairs(src, dst, device):
+    _on(src, "src", device)
+    n = src.numel()
+    _ints(src, "src", (n,), device)
+    _ints(dst, "dst", (n,), device)
+    return n
+
+
 def _ws(op, c, n, device):
     need = lib().pbs_cache_workspace_bytes(c, op, n)
     return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
@@ -299,9 +309,7 @@ def cache_copy(k_pages, v_pages, src, dst):
     device."""
     c = _pools(k_pages, v_pages)
     dev = k_pages.device
-    _ints(src, "src", (src.numel(),), dev)
-    _ints(dst, "dst", (src.numel(),), dev)
-    n = src.numel()
+    n = _pairs(src, dst, dev)
     ws, need = _ws(_lib.CACHE_COPY, c, n, dev)
     _call("pbs_cache_copy", dev, _ptr(k_pages), _ptr(v_pages), _ptr(src), _ptr(dst), n, c,
           _ptr(ws), need)
@@ -312,10 +320,9 @@ def cache_fork(table, refs, lens, src, dst, page):
     pages (pbs_cache_fork); no page is copied before one of them writes."""
     c = _books(table, refs, lens, page)
     dev = table.device
-    _ints(src, "src", (src.numel(),), dev)
-    _ints(dst, "dst", (src.numel(),), dev)
+    n = _pairs(src, dst, dev)
     _call("pbs_cache_fork", dev, _ptr(table), _ptr(refs), _ptr(lens), _ptr(src), _ptr(dst),
-          src.numel(), c)
+          n, c)
 
 
 def cache_trim(table, refs, lens, keep, page):
@@ -343,13 +350,13 @@ def cache_compact(k_pages, v_pages, table, refs):
 def cache_accept(k_pages, v_pages, table, start, path, count=None, lens=None):
     """The accepted drafts moved behind their prefix: token start[s] +
     path[s][i] becomes token start[s] + i, i < count[s], in every layer
-    (pbs_cache_accept). path [seqs, tree] ascends strictly. With ``lens``,
-    lens[s] becomes start[s] + count[s]."""
+    (pbs_cache_accept). path [seqs, n] ascends strictly (n may be less than the
+    drafts). With ``lens``, lens[s] becomes start[s] + count[s]."""
     c = _pools(k_pages, v_pages, table)
     dev = k_pages.device
     _ints(start, "start", (c.seqs,), dev)
     if not isinstance(path, torch.Tensor) or path.dim() != 2:
-        raise ValueError("path must be [seqs, tree]")
+        raise ValueError("path must be [seqs, n]")
     _ints(path, "path", (c.seqs, path.shape[1]), dev)
     for t, nm in ((count, "count"), (lens, "lens")):
         if t is not None:

@@ -101,6 +101,9 @@ def test_rope_freqs_scalings():
 @pytest.mark.parametrize("kw", [dict(rot=24), dict(rot=-16), dict(rot=64, base=0.0),
                                 dict(rot=64, scaling=dict(type="linear", factor=0.5)),
                                 dict(rot=64, scaling=dict(type="other", factor=2)),
+                                dict(rot=64, base=1.0), dict(rot=64, scaling=dict(factor=2)),
+                                dict(rot=64, scaling=dict(type="linear")),
+                                dict(rot=64, scaling=dict(type="yarn", factor=2)),
                                 dict(rot=64, scaling=dict(type="linear", factor=2, low=1)),
                                 dict(rot=64, scaling=dict(type="ramp", factor=2, original=8,
                                                           low=4, high=4))])
@@ -236,6 +239,9 @@ def test_binding_refuses_host_tensors():
         pbs.tree_attn(x, x, x, torch.zeros(1, 2, dtype=torch.int32), i[:1])
     with pytest.raises(TypeError):
         pbs.rope([1.0], None, i, f)
+    for bad in ((x, [0], i), (x, i, i)):
+        with pytest.raises((TypeError, ValueError)):
+            pbs.cache_copy(x, *bad)
     with pytest.raises(ValueError):
         pbs.PagedCache(0, 16, 4, 2, 64, device="cpu")
 

@@ -329,7 +329,7 @@ def test_append_and_accept_refuse_pages_they_do_not_have(dev):
     lens = i32([7, 8, 9], dev)
     for start, path in (([14, 0, 31], [[1, 2], [0, 1], [1, 2]]),      # pages missing
                         ([0, 0, -1], [[1, 1], [1, 0], [0, 1]]),       # does not ascend; start < 0
-                        ([0, 0, 0], [[-1, 1], [2, 3], [0, 3]])):      # outside the tree
+                        ([0, 0, 0], [[-1, 1], [2, 3], [0, 32]])):     # before, a bad page, behind
         pbs.cache_accept(k, v, table, i32(start, dev), i32(path, dev)[:, :2].contiguous(),
                          lens=lens)
         assert pbs.device_status() == _lib.ERR_DEVICE_ASSERT
@@ -637,6 +637,105 @@ def test_many_items_in_a_run(tree, hq, hkv, b, most, dev):
         tol = half_step(BF16) * (p @ vv).abs() + 2 * half_step(BF16) * (p @ vv.abs())
         assert ((o[s, :, :c].double() - p @ vv).abs() <= tol).all()
         assert (lse[s, :, :c].double() - torch.logsumexp(a, -1)).abs().max() < 1e-3
+
+
+@pytest.mark.parametrize("tree,g", [(1, 4), (7, 4), (64, 4)])
+def test_waits_are_bounded(tree, g, dev, monkeypatch):
+    """Each kernel with every CTA's first K tile left out: the waits run out
+    (about a second), the status says so, and the next call is right."""
+    t = Tree(dev, BF16, 128, 64, 1, [300], [tree], tree, junk=False)
+    q = torch.randn(1, g, tree, 128, device=dev).to(BF16)
+    call = lambda: pbs.tree_attn(q, t.k, t.v, t.table, i32(t.start, dev))
+    good = call()
+    assert pbs.device_status() == 0
+    monkeypatch.setenv("PBS_FAULT_INJECT", "tree")
+    call()
+    code, where = pbs.device_status(detail=True)
+    monkeypatch.delenv("PBS_FAULT_INJECT")
+    assert code == _lib.ERR_TIMEOUT and where > 0
+    assert torch.equal(call(), good)
+
+
+def test_pools_beyond_32_bits(dev):
+    """Pools of 4.5 GB each: copies, appends, accepts and attention at pages
+    whose offsets pass 2^31 elements and 2^32 bytes."""
+    hkv, page, d = 8, 64, 128
+    pages = 2 ** 31 // (hkv * page * d) + 3000
+    k, v = (torch.empty(pages, hkv, page, d, dtype=BF16, device=dev) for _ in range(2))
+    top = [pages - 1, pages - 2, pages - 700]
+    n, t = 150, 3
+    table = i32([top], dev)
+    rows = [torch.randn(1, hkv, n + t, d, device=dev).to(BF16) for _ in range(2)]
+    pbs.cache_append(*rows, k, v, table, i32([0], dev))
+    q = torch.randn(1, hkv * 2, t, d, device=dev).to(BF16)
+    o = pbs.tree_attn(q, k, v, table, i32([n], dev))
+    flat = [x.double().repeat_interleave(2, 1) for x in rows]
+    a = q.double() @ flat[0].transpose(2, 3) / math.sqrt(d)
+    a += torch.full((t, n + t), -math.inf, device=dev, dtype=torch.float64).triu(n + 1)
+    p = torch.softmax(a, -1)
+    tol = half_step(BF16) * (p @ flat[1]).abs() + 2.0 ** -10 * (p @ flat[1].abs())
+    assert ((o.double() - p @ flat[1]).abs() <= tol).all()
+    pbs.cache_copy(k, v, table[0].contiguous(), i32([0, 1, pages - 5], dev))
+    assert torch.equal(bits(k[top]), bits(k[[0, 1, pages - 5]]))
+    assert torch.equal(bits(v[top]), bits(v[[0, 1, pages - 5]]))
+    pbs.cache_accept(k, v, table, i32([n], dev), i32([[0, 2]], dev))
+    got = k[top].transpose(0, 1).reshape(hkv, -1, d)
+    assert torch.equal(got[:, n + 1], rows[0][0, :, n + 2])
+    m = k.clone()[:4]  # keep four pages, then compact the top ones down
+    refs = torch.zeros(pages, dtype=torch.int32, device=dev)
+    refs[top] = 1
+    want = [x[top].clone() for x in (k, v)]
+    pbs.cache_compact(k, v, table, refs)
+    assert sorted(table[0].tolist()) == [0, 1, 2] and refs[:3].tolist() == [1, 1, 1]
+    for x, w in zip((k, v), want):
+        assert torch.equal(bits(x[table[0].long()]), bits(w))
+    del m
+
+
+def test_cache_calls_in_a_graph(dev):
+    """Reserve, copy, append, attend, accept and trim captured together and
+    replayed: each replay works on what the tables hold by then."""
+    hkv, d, page = 2, 64, 16
+    c = pbs.PagedCache(3, 200, 64, hkv, d, page, 1, BF16, dev)
+    count, want, keep = i32([2, 2, 0], dev), i32([2, 2, 0], dev), i32([-1, -1, -1], dev)
+    k, v = (torch.zeros(3, hkv, 2, d, dtype=BF16, device=dev) for _ in range(2))
+    q = torch.zeros(3, 4, 2, d, dtype=BF16, device=dev)
+    path, taken = i32([[1, 0], [0, 1], [0, 0]], dev), i32([1, 2, 0], dev)
+
+    def step():
+        c.reserve(want)
+        c.append(0, k, v, count=count)
+        o = c.attend(0, q, count=count)
+        c.accept(path, taken)
+        c.trim(keep)
+        return o
+
+    side = torch.cuda.Stream(dev)
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    c.trim(i32([0, 0, 0], dev))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    rows = [[], []]
+    g = torch.Generator().manual_seed(3)
+    for i in range(20):
+        for x in (k, v, q):
+            x.copy_(torch.randn(x.shape, generator=g).to(BF16))
+        want.copy_(torch.where(count > 0, c.lens + 2, 0))
+        graph.replay()
+        for s in (0, 1):
+            kk, vv = (np.concatenate([rows[s][j], f64(x[s])], 1) if len(rows[s]) else f64(x[s])
+                      for j, x in enumerate((k, v)))
+            n = kk.shape[1] - 2
+            for h in range(4):
+                w = dec.attend(f64(q[s, h]), kk[h // 2], vv[h // 2], n, np.tril(np.ones((2, 2), bool)),
+                               1 / 8)[0]
+                assert np.abs(f64(out[s, h]) - w).max() <= 2.0 ** -8 * np.abs(w).max() + 2.0 ** -9
+            at = list(range(n)) + [n + j for j in ([1], [0, 1])[s]]
+            rows[s] = [kk[:, at], vv[:, at]]
+    assert c.lens.tolist() == [20, 40, 0] and pbs.device_status() == 0
 
 
 def test_tree_attn_refuses(dev):
