@@ -586,8 +586,8 @@ pbs_status pbs_tree_mask(const int32_t *parents, uint32_t *mask, int32_t *depth,
  * 0 .. start[s]-1 and those tokens start[s] + j, j < count[s], whose bit is
  * set in mask row i (mask NULL: j <= i, a chain). With tree == 1 this is a
  * decoding step. Logits sigma * q . k, the softmax's maximum and sum and the
- * output's sums are fp32; the weights are rounded to 16 bits for the second
- * product (with hq / hkv * tree <= 16 they keep two 16-bit parts).
+ * output's sums are fp32; the weights are rounded to 16 bits for the product
+ * with V.
  *
  *   q    [seqs, hq, tree, d] (layer stride unused), bf16 or fp16
  *   k_pages, v_pages [pages, hkv, page, d]: one layer (c.layers is ignored);

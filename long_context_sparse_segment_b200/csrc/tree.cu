@@ -223,9 +223,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 if (!(seen >> (n * 8 + e) & 1)) s[n][2 * x + e] = -INFINITY;
           }
         }
-        // running maximum, P in two 16-bit parts: 16 bits alone would add as
-        // much error as the output's own rounding
-        uint32_t hi[4], lo[4];
+        // running maximum; P rounded to 16 bits (see tree.cuh)
+        uint32_t p[4];
         float alpha[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -242,10 +241,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const float p0 = ex2_approx(fmaf(s[n][2 * x], a.sl2, -mu));
             const float p1 = ex2_approx(fmaf(s[n][2 * x + 1], a.sl2, -mu));
             sum += p0 + p1;
-            const uint32_t w = Two<T>::pack(p0, p1);
-            const float2 f = Two<T>::unpack(w);
-            hi[2 * n + x] = w;
-            lo[2 * n + x] = Two<T>::pack(p0 - f.x, p1 - f.y);
+            p[2 * n + x] = Two<T>::pack(p0, p1);
           }
           l[x] = l[x] * alpha[x] + sum;
         }
@@ -283,10 +279,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           }
 #pragma unroll
           for (int y = 0; y < 4; ++y)
-            Two<T>::mma(o[2 * n + y], hi, b[y >> 1][2 * (y & 1)], b[y >> 1][2 * (y & 1) + 1]);
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            Two<T>::mma(o[2 * n + y], lo, b[y >> 1][2 * (y & 1)], b[y >> 1][2 * (y & 1) + 1]);
+            Two<T>::mma(o[2 * n + y], p, b[y >> 1][2 * (y & 1)], b[y >> 1][2 * (y & 1) + 1]);
         }
       }
       warp_arrive(&bar->empty[st], lane);

@@ -9,6 +9,12 @@
 // sum and output (fp32) in the workspace, at most two per CTA, and the
 // combining kernel joins them in unit order, so results do not depend on
 // timing.
+//
+// The weights P are rounded to 16 bits for the product with V; their sum takes
+// the unrounded ones. A weight is off by half a step at most, independently
+// from key to key, so the output gains about as much error as its own rounding
+// has (1.4 times it together). A second 16-bit part would take that away: under
+// the power limit it cost 5 % of a decoding step and 10 % of 7 drafts over 128K.
 #pragma once
 
 #include <cuda.h>
@@ -222,9 +228,6 @@ struct Two;
 template <>
 struct Two<__nv_bfloat16> {
   static __device__ __forceinline__ uint32_t pack(float x, float y) { return pack_bf16(x, y); }
-  static __device__ __forceinline__ float2 unpack(uint32_t u) {
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-  }
   static constexpr uint32_t kExp = 0x7f80u;
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
@@ -236,9 +239,6 @@ struct Two<__half> {
   static __device__ __forceinline__ uint32_t pack(float x, float y) {
     const __half2 v = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&v);
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t u) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
   }
   static constexpr uint32_t kExp = 0x7c00u;
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,

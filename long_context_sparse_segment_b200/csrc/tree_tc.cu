@@ -17,10 +17,6 @@
 //   warps 4-11  the softmax of the two streams, Q into shared memory, the
 //               item's end.
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (D each).
-//
-// P is rounded to 16 bits for the second product: its relative error (half a
-// step per weight, independent from key to key) is as large as the output's
-// own rounding, no more; the sum l takes the unrounded weights.
 #include "internal.h"
 #include "tree_tc.h"
 
@@ -36,7 +32,6 @@ constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168, kCtrlRegs = 56, kSoftmaxRegs = 224;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split");
 constexpr float kRescaleLog2 = 8.f;  // the running maximum moves by more than 2^8 or not at all
-constexpr int kSingleParts = 2;
 constexpr int kBadSlots = 8;         // segments in flight, at most kVS + 2
 
 template <int D, bool PAIR>
@@ -44,7 +39,6 @@ struct Cfg {
   static constexpr int H = D / 64;
   static constexpr int ROWS = PAIR ? 256 : 128;
   static constexpr uint32_t TILE = kTile * D * 2, HALF = kTile * 128;
-  static constexpr int PARTS = PAIR ? 1 : kSingleParts;  // 16-bit parts of P
   static constexpr int KS = D == 64 ? 5 : 2, VS = D == 64 ? 5 : 3;
   static_assert(VS + 2 < kBadSlots, "bad flags");
   struct Shared {
@@ -267,9 +261,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int kk = h * 4 + k2;
               mma_ts(tbase + 256 + x * 128, tbase + x * 128 + kk * 8,
                      desc_words(lv + kk * (2048 >> 4), hi), kIdPV, add || kk > 0);
-              if (C::PARTS == 2)
-                mma_ts(tbase + 256 + x * 128, tbase + x * 128 + 64 + kk * 8,
-                       desc_words(lv + kk * (2048 >> 4), hi), kIdPV, 1);
             }
           }
           __syncwarp();
@@ -488,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        make_float2(0.f, 0.f)};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16], rest[16];
+        uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[c * 32 + 2 * e]),
@@ -497,13 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
           acc[e & 3] = __fadd2_rn(acc[e & 3], p);
           pk[e] = Two<T>::pack(p.x, p.y);
-          if (C::PARTS == 2) {
-            const float2 r = Two<T>::unpack(pk[e]);
-            rest[e] = Two<T>::pack(p.x - r.x, p.y - r.y);
-          }
         }
         tmem_st16(tS + c * 16, pk);
-        if (C::PARTS == 2) tmem_st16(tS + 64 + c * 16, rest);
         if (c & 1) {
           tmem_wait_st();
           tc_fence_before();
