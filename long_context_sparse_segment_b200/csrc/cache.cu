@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int sh[33];
   const int tid = threadIdx.x, lane = tid & 31;
   int lo, hi, live, n, skip;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   warp_run(c.pages, &lo, &hi);
   n = 0;
 #pragma unroll 4
@@ -281,17 +282,6 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (tid == 0) *moves = n;
 }
 
-__global__ void __launch_bounds__(256)
-    remap_kernel(int32_t *table, const int32_t *__restrict__ to, int64_t n, int pages) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int e = table[i];
-    if (e >= 0 && e < pages) {
-      const int t = to[e];
-      if (t != e) table[i] = t;
-    }
-  }
-}
-
 // --------------------------------------------------------------- page copies
 // Pairs up to this many are checked against each other by every CTA (4 KB of
 // reads from L2); more go through an owner table.
@@ -306,22 +296,34 @@ __global__ void __launch_bounds__(256)
   if (i < n && dst[i] >= 0 && dst[i] < pages) atomicMin((unsigned *)owner + dst[i], (unsigned)i);
 }
 
-// One CTA per piece of (pair, pool, layer). `count` (device, may be null)
-// bounds the pairs of a compaction, whose pairs are sound by construction
-// and whose CTAs walk them; otherwise gridDim.y covers the pairs.
+// The CTAs walk the pieces of every (pair, pool, layer). COMPACT: the pairs are
+// a compaction's, sound by construction, `count` of them, and the CTAs first
+// put the pages' new places `to` into the table; the kernel is launched while
+// the plan still runs and waits for it here.
+template <bool COMPACT>
 __global__ void __launch_bounds__(kCopyThreads)
-    copy_kernel(uint4 *k, uint4 *v, const int32_t *__restrict__ src,
-                const int32_t *__restrict__ dst, int n, const int32_t *__restrict__ count,
-                const int32_t *__restrict__ owner, pbs_cache c, int64_t page_words, int pieces,
-                int *err) {
+    copy_kernel(uint4 *k, uint4 *v, const int32_t *src, const int32_t *dst, int n,
+                const int32_t *count, const int32_t *to_page, int32_t *table,
+                const int32_t *owner, pbs_cache c, int64_t page_words, int pieces, int *err) {
   const int tid = threadIdx.x;
   const int64_t per_pair = 2LL * c.layers * pieces;
-  const int pairs = count ? *count : n;
+  if (COMPACT) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t entries = (int64_t)c.seqs * c.width;
+    for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + tid; i < entries;
+         i += (int64_t)gridDim.x * kCopyThreads) {
+      const int e = table[i];
+      if (e < 0 || e >= c.pages) continue;
+      const int t = to_page[e];
+      if (t != e) table[i] = t;
+    }
+  }
+  const int pairs = COMPACT ? *count : n;
   for (int64_t w = blockIdx.x; w < per_pair * pairs; w += gridDim.x) {
     const int i = (int)(w / per_pair), part = (int)(w - i * per_pair);
     const int a = src[i], b = dst[i];
     if (a < 0 && b < 0) continue;
-    if (!count) {
+    if (!COMPACT) {
       bool bad = a < 0 || b < 0 || a >= c.pages || b >= c.pages;
       if (!bad && owner) {
         bad = owner[b] != i || owner[a] != -1;
@@ -547,9 +549,9 @@ pbs_status pbs_cache_copy(void *k_pages, void *v_pages, const int32_t *src, cons
     if (cudaMemsetAsync(owner, 0xff, need, cs) != cudaSuccess) return PBS_ERR_CUDA;
     owner_kernel<<<n / 256 + 1, 256, 0, cs>>>(dst, n, c.pages, owner);
   }
-  copy_kernel<<<copy_grid(c, n), kCopyThreads, 0, cs>>>((uint4 *)k_pages, (uint4 *)v_pages, src,
-                                                       dst, n, nullptr, owner, c, page_words(c),
-                                                       pieces(c), error_word());
+  copy_kernel<false><<<copy_grid(c, n), kCopyThreads, 0, cs>>>(
+      (uint4 *)k_pages, (uint4 *)v_pages, src, dst, n, nullptr, nullptr, nullptr, owner, c,
+      page_words(c), pieces(c), error_word());
   return done();
 }
 
@@ -584,14 +586,21 @@ pbs_status pbs_cache_compact(void *k_pages, void *v_pages, int32_t *table, int32
   cudaStream_t cs = (cudaStream_t)st;
   int32_t *to = (int32_t *)ws, *moves = to + c.pages;
   compact_kernel<<<1, kPlanThreads, 0, cs>>>(refs, move_src, move_dst, c, to, moves);
-  const int64_t entries = (int64_t)c.seqs * c.width, blocks = ceil_div(entries, 256);
-  if (entries)
-    remap_kernel<<<(unsigned)(blocks < 148 * 8 ? blocks : 148 * 8), 256, 0, cs>>>(table, to,
-                                                                                  entries, c.pages);
-  copy_kernel<<<copy_grid(c, c.pages / 2 + 1), kCopyThreads, 0, cs>>>(
-      (uint4 *)k_pages, (uint4 *)v_pages, move_src, move_dst, c.pages, moves, nullptr, c,
-      page_words(c), pieces(c), error_word());
-  return done();
+  if (cudaGetLastError() != cudaSuccess) return PBS_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(copy_grid(c, c.pages / 2 + 1));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = cs;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, copy_kernel<true>, (uint4 *)k_pages, (uint4 *)v_pages, (const int32_t *)move_src,
+      (const int32_t *)move_dst, c.pages, (const int32_t *)moves, (const int32_t *)to, table,
+      (const int32_t *)nullptr, c, page_words(c), pieces(c), error_word());
+  return e == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
 }
 
 pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,

@@ -52,12 +52,6 @@ def _ints(t, name, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _dense(t):
-    """A contiguous [b, h, n, d] as pbs_rows."""
-    _, h, n, d = t.shape
-    return Rows(t.data_ptr(), 0, h * n * d, n * d, d)
-
-
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -164,50 +158,54 @@ def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=No
     turns back: the gradients of q and k from those of the results. Returns
     (q', k'), or q' alone without k. q_out, k_out may be q and k themselves."""
     _on(q, "q")
-    dev = q.device
-    if q.dim() != 4:
+    dev, t, size = q.device, q.dtype, q.shape
+    kind, order = _TYPES.get(t), _LAYOUTS.get(layout)
+    if len(size) != 4:
         raise ValueError("q must be [b, hq, n, d]")
-    if q.dtype not in _TYPES:
-        raise TypeError(f"q must be bf16, fp16 or fp32, got {q.dtype}")
-    if layout not in _LAYOUTS:
+    if kind is None:
+        raise TypeError(f"q must be bf16, fp16 or fp32, got {t}")
+    if order is None:
         raise ValueError(f"layout must be 'half' or 'pairs', got {layout!r}")
-    b, hq, n, d = q.shape
+    b, hq, n, d = size
     if d < 16 or d % 16 or d > 1024:
         raise ValueError("the head dimension must be a multiple of 16, at most 1024")
+    hkv = 0
     if k is not None:
         _on(k, "k", dev)
-        if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (b, n, d) or k.dtype != q.dtype:
+        ksize = k.shape
+        if len(ksize) != 4 or (ksize[0], ksize[2], ksize[3]) != (b, n, d) or k.dtype is not t:
             raise ValueError("k must be [b, hkv, n, d] of q's type")
+        hkv = ksize[1]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     _on(inv_freq, "inv_freq", dev)
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous fp64 vector")
     rot = 2 * inv_freq.numel()
     if rot % 16 or rot > d:
         raise ValueError("inv_freq: 2 * len must be a multiple of 16 and at most d")
-    _ints(pos, "pos", (n,) if isinstance(pos, torch.Tensor) and pos.dim() == 1 else (b, n), dev)
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
-    outs = []
-    for x, y, nm in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+    each = isinstance(pos, torch.Tensor) and pos.dim() == 1
+    _ints(pos, "pos", (n,) if each else (b, n), dev)
+    outs, rows = [], []
+    for x, y, h, nm in ((q, q_out, hq, "q"), (k, k_out, hkv, "k")):
         if x is None:
+            rows += (_NONE, _NONE)
             continue
-        if y is not None:
-            _on(y, nm, dev)
-            if y.shape != x.shape or y.dtype != x.dtype:
-                raise ValueError(f"{nm} must have the shape and type of its input")
-        outs.append(_fresh(x) if y is None else y)
-    hkv = 0 if k is None else k.shape[1]
+        if y is None:
+            new = _fresh(x)
+            to = Rows(new.data_ptr(), 0, h * n * d, n * d, d)
+        else:
+            new = y
+            _on(y, nm + "_out", dev)
+            if y.shape != x.shape or y.dtype is not t:
+                raise ValueError(f"{nm}_out must have the shape and type of its input")
+            to = _rows(y, nm + "_out", True) if y.numel() else _NONE
+        outs.append(new)
+        rows += (_rows(x, nm) if x.numel() else _NONE, to)
     if b and n and hq + hkv:
-        qr = kr = qo = ko = _NONE
-        if hq:
-            qr = _rows(q, "q")
-            qo = _dense(outs[0]) if q_out is None else _rows(q_out, "q_out", True)
-        if hkv:
-            kr = _rows(k, "k")
-            ko = _dense(outs[1]) if k_out is None else _rows(k_out, "k_out", True)
-        _call("pbs_rope", dev, qr, qo, hq, kr, ko, hkv, _ptr(pos), 0 if pos.dim() == 1 else n,
-              _ptr(inv_freq), gain, b, n, d, rot, _LAYOUTS[layout], int(bool(transpose)),
-              _TYPES[q.dtype])
+        _call("pbs_rope", dev, rows[0], rows[1], hq, rows[2], rows[3], hkv, pos.data_ptr(),
+              0 if each else n, inv_freq.data_ptr() if rot else None, gain, b, n, d, rot, order,
+              1 if transpose else 0, kind)
     return outs[0] if k is None else tuple(outs)
 
 
