@@ -40,7 +40,7 @@ struct MmaCfg {
   static constexpr int PAD = 4;                   // floats behind a joined row
   static constexpr size_t JOIN = (size_t)kConsumers * RJ * (D + PAD) * 4;
   struct Bars {
-    uint64_t full[ST], empty[ST], q_full[2], q_empty[2], join;
+    uint64_t full[ST], empty[ST], q_full[2], q_empty[2];
     int abort;
     int bad[kConsumers];
     Segment g[2];
@@ -72,7 +72,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       mbar_init(&bar->q_full[i], 33);  // each lane's copies, and the segment
       mbar_init(&bar->q_empty[i], kConsumers);
     }
-    mbar_init(&bar->join, kConsumers);
     bar->abort = 0;
     fence_barrier_init();
   }
@@ -88,7 +87,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     // Finds the segments, brings each one's Q rows (a segment ahead of the
     // consumers, as the ring allows) and its units: up to 4 pieces of pages,
     // K and V, one lane each. Rows of a page behind the last token come along;
-    // pages behind it do not. A unit's page numbers are read one unit early.
+    // pages behind it do not. The table is read 32 entries at a time, 32 early:
+    // one entry a unit early held a unit to the latency of L2 (700 cycles, more
+    // than the 64 keys of d = 64 take to arrive).
     Walk<ROWS, kKeys> walk(place);
     Segment g;
     const int kv = lane & 1, piece = lane >> 1, shift = 31 - __clz(a.page);
@@ -120,12 +121,17 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       const int len = g.start + g.count;
       const int32_t *row = a.table + (size_t)g.s * a.width;
       int t = g.k0 * kKeys + piece * box;
-      auto page_of = [&](int tok) { return mine && tok < len ? __ldg(row + (tok >> shift)) : 0; };
-      int page = page_of(t);
+      const int last = (min(len, g.k1 * kKeys) - 1) >> shift;  // column
+      int col = g.k0 * kKeys >> shift;                         // of lane 0's entry
+      auto entry = [&](int c) { return c + lane <= last ? __ldg(row + c + lane) : 0; };
+      int held = entry(col), ahead = entry(col + 32);
       for (int k = g.k0; k < g.k1; ++k, ++it, t += kKeys) {
         const int st = it % ST;
         const bool load = mine && t < len;
-        const int ahead = k + 1 < g.k1 ? page_of(t + kKeys) : 0;
+        // a unit's columns never straddle the 32: both begin at multiples of
+        // the columns of a unit
+        if ((k * kKeys >> shift) - col >= 32) col += 32, held = ahead, ahead = entry(col + 32);
+        int page = __shfl_sync(0xffffffffu, held, ((t >> shift) - col) & 31);
         if (load && (page < 0 || page >= a.pages)) {
           report(a.err, PBS_ERR_DEVICE_ASSERT);
           page = 0;
@@ -142,7 +148,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           tma_load_3d(ring + (size_t)(2 * st + kv) * C::KV + piece * box * D * 2,
                       kv ? &tmV : &tmK, &bar->full[st], 0, y, 0);
         __syncwarp();
-        page = ahead;
       }
     }
     // every copy started here lands before the CTA exits
@@ -156,18 +161,28 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   // --------------------------------------------------------------- consumers
   const int half_id = warp >> 2, key16 = (warp & 3) * 16;
   const int gr = lane >> 2, qc = (lane & 3) * 2;
-  uint32_t phase = 0;
-  auto sync = [&]() {  // the eight warps
-    warp_arrive(&bar->join, lane);
-    const bool ok = mbar_wait_warp(&bar->join, phase, abort, a.err, 51);
-    phase ^= 1;
-    return ok;
+  // The eight warps meet in named barriers (a bounded mbarrier wait instead costs
+  // 0.2 us each, up to eight an item). So a warp whose wait ran out goes on to
+  // every barrier of the segment, and all leave together at the next one.
+  auto sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+  bool failed = false;
+  auto agree = [&]() {
+    int any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, 256, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((int)failed)
+        : "memory");
+    failed = any != 0;
   };
   const uint32_t half_bytes = box * 128;  // from one column half to the other
   const uint32_t key_bytes = key16 / box * (box * D * 2) + key16 % box * 128;
   int it = 0;
   for (int seg = 0;; ++seg) {
-    if (!mbar_wait_warp(&bar->q_full[seg & 1], seg >> 1 & 1, abort, a.err, 42)) return;
+    if (!mbar_wait_warp(&bar->q_full[seg & 1], seg >> 1 & 1, abort, a.err, 42)) failed = true;
+    agree();  // also: the join buffer's last readers are through
+    if (failed) return;
     const Segment g = bar->g[seg & 1];
     if (g.count == 0) return;
     const int rows = min(ROWS, g.count * a.G - g.rt * ROWS);  // of this row tile
@@ -189,10 +204,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     for (int k = g.k0; k < g.k1; ++k, ++it) {
       if ((it & 1) != half_id) continue;
       const int st = it % ST;
-      if (!mbar_wait_warp(&bar->full[st], (it / ST) & 1, abort, a.err, 41)) return;
+      if (!failed && !mbar_wait_warp(&bar->full[st], (it / ST) & 1, abort, a.err, 41))
+        failed = true;
       const uint8_t *tK = ring + (size_t)(2 * st) * C::KV + key_bytes, *tV = tK + C::KV;
       const int key0 = k * kKeys + key16;  // this warp's 16 keys
-      if (key0 < len) {
+      if (key0 < len && !failed) {
         // S = Q K^T
         float s[2][4];
 #pragma unroll
@@ -301,7 +317,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       return x;
     };
     for (int r0 = 0; r0 < rows; r0 += RJ) {
-      if (!sync()) return;  // the buffer's last readers are through
+      if (r0 > 0) sync();  // the buffer's last readers are through
       if (r0 == 0) {
         if (lane == 0) bar->bad[warp] = bad;
 #pragma unroll
@@ -316,7 +332,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           for (int n = 0; n < D / 8; ++n)
             *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
         }
-      if (!sync()) return;
+      sync();
       const int r = r0 + tid % RJ, col = tid / RJ * N;
       if (r < rows) {
         float top = -INFINITY;
