@@ -284,7 +284,10 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // --------------------------------------------------------------- page copies
 // Pairs up to this many are checked against each other by every CTA (4 KB of
-// reads from L2); more go through an owner table.
+// reads from L2); more go through an owner table, a memset and a launch more:
+// 512 pairs of 4 KB take 5.5 us scanned and 5.0 by the table, but the host 5 us
+// longer; 8000 pairs 92 us scanned and 58 by the table. The copies themselves
+// run at the copy rate: 96 pages of 32 layers (1.6 GB read and written) 249 us.
 constexpr int kScanPairs = 512;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;  // 16-byte loads in flight per thread

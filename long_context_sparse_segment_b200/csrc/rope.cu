@@ -5,7 +5,11 @@
 // The work is one read and one write of every element, so the kernel is
 // bound by memory (small batches: by latency). A token's angles are the
 // same in every head: a thread computes the cosines and sines of its pairs
-// once and walks the heads with them.
+// once and walks the heads with them, four heads' reads in flight (one at a
+// time 123 us, two 112, four 109, eight 133 for 32768 tokens of 32 + 8 heads, d =
+// 128, where 671 MB at the copy rate take 102): 6.1 TB/s. 256 threads a block
+// write 8 KB in a row of each head (128 threads: 3 % slower, 512: 18 %). A step
+// of 16 tokens takes 2.5 us on the device.
 //
 // Angles. t f in fp32 is off by up to t f 2^-24 radians (0.008 at 131072),
 // more than a bf16 result's rounding, and fp64 sine and cosine are slow. So
@@ -190,7 +194,8 @@ extern "C" pbs_status pbs_rope(pbs_rows q, pbs_rows q_out, int hq, pbs_rows k, p
   const int64_t bx = ceil_div(a.tokens * (d * elem / 32), kThreads);
   if (bx > 0x7fffffff) return PBS_ERR_UNSUPPORTED;
   // few tokens: the heads are split over blocks until there are sixteen blocks
-  // an SM, and the angles computed again in each
+  // an SM, and the angles computed again in each (12252 tokens of 15 fp32 heads:
+  // 33.7 us, with eight blocks an SM 35.8)
   int64_t split = ceil_div(148 * 16, bx);
   if (split > a.heads) split = a.heads;
   a.heads_per = (int)ceil_div(a.heads, split);

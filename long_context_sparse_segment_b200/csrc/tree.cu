@@ -11,7 +11,13 @@
 // This kernel: up to 16 rows an item, warp MMA. Eight warps take tiles of 64
 // keys, four warps a tile (16 keys each) and the two halves in turn, each
 // with its own maximum, sum and output, joined when the item ends; a ninth
-// warp brings the tiles by TMA, page by page, into a ring.
+// warp brings the tiles by TMA, page by page, into a ring. A unit keeps a warp
+// busy for 1,450 cycles, two warps a scheduler, while its 32 KB (d = 128) take
+// 1,450 to arrive at the copy rate: the tensor core of tcgen05 would have 4 to
+// 16 of its 128 rows to do. Measured: a new token of each of 48 sequences of
+// 100 to 32768 tokens (3.29 GB of K and V) 493-509 us, 6.5-6.7 TB/s (the copy
+// rate is 6.56); one sequence of 8192 tokens 17 us, of which the bytes are 5
+// and the rest launches, the run's start and the combining kernel.
 #include <stdlib.h>
 #include <string.h>
 
@@ -30,7 +36,6 @@ constexpr int kMmaThreads = 32 * (kConsumers + 1);
 
 template <int D>
 struct MmaCfg {
-  static constexpr int H = D / 64;
   static constexpr int ROWS = 16;
   static constexpr uint32_t KV = kKeys * D * 2;   // bytes of a K or V tile
   // 192 KB in flight an SM (128 KB: 6 % slower on a ragged batch, 64 KB: 30 %);
@@ -56,7 +61,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     tree_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a) {
   using C = MmaCfg<D>;
-  constexpr int H = C::H, ST = C::ST, ROWS = C::ROWS;
+  constexpr int ST = C::ST, ROWS = C::ROWS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -431,6 +436,20 @@ bool tree_supported(int hq, int tree, const pbs_cache &c) {
                  (ceil_div((int64_t)c.width * c.page, kKeys) + kExtra<256>) < 2e9;
 }
 
+// The rows of an item: 16 by warp MMA, 128 or 256 (in pairs) by tcgen05, by the
+// most rows that a KV head can have. Both sides, us a call (32 / 8 heads, d =
+// 128, 64-token pages):
+//   rows, sequences x tokens    16 by MMA   128 alone   256 in pairs
+//   4    8 x 16K                     91.9        89.4          -
+//   16   8 x 16K                     96.2        90.2          -
+//   4    64 x 1000                   53.8        75.4          -
+//   16   64 x 1000                   65.7        75.6          -
+//   4    1 x 8K                      17.2        20.0          -
+//   32   8 x 16K                        -        94.1      107.5
+//   128  8 x 16K                        -       105.6      114.8
+//   192  8 x 16K                        -       183.1      152.5
+//   256  8 x 16K                        -       191.4      162.5
+// (the lengths, which would settle 4 to 16 rows, are on the device).
 int row_tile(int hq, int tree, const pbs_cache &c) {
   const int64_t rows = (int64_t)(hq / c.hkv) * tree;
   return rows <= 16 ? 16 : rows <= 128 ? 128 : 256;

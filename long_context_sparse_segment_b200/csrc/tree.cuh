@@ -71,7 +71,9 @@ __device__ __forceinline__ int cdiv(int x, int y) { return (x + y - 1) / y; }
 // What an item's beginning and end cost a CTA, in key tiles: so many units are
 // counted in front of an item's own, and a run that begins an item gets fewer
 // tiles. Measured with clocks in the kernels: 7 us of 1.9 us tiles (256 rows),
-// 5 of 1.6 (128 rows), 1.5 of 0.7 (16 rows, 64 keys).
+// 5 of 1.6 (128 rows), 1.5 of 0.7 (16 rows, 64 keys). Without it 7 drafts over
+// 128K tokens take 110 instead of 106 us, 64 drafts of 64 sequences of 1000
+// tokens 166 instead of 160; twice as much changes nothing more.
 template <int ROWS>
 constexpr int kExtra = ROWS == 16 ? 2 : 3;
 
@@ -112,7 +114,7 @@ __device__ __forceinline__ bool find_place(const TreeArgs &a, int *sum, Place *p
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto units = [&](int s) { return s < a.seqs ? units_of<ROWS, KEYS>(a, seq_of(a, s)) : 0; };
   // up to 32 sequences a warp holds them all and nobody waits for another; more
-  // are summed by the block first
+  // are summed by the block first (a barrier and a second look at the lengths)
   int x = units(a.seqs <= 32 ? lane : tid), total = x;
   if (a.seqs > 32) {
     for (int s = tid + NT; s < a.seqs; s += NT) total += units(s);
@@ -304,17 +306,17 @@ __device__ __forceinline__ void write_row(const TreeArgs &a, int s, int h, int r
   T *dst = (T *)a.out + (((size_t)s * a.hq + h * a.G + g) * a.tree + i) * d + col;
   if constexpr (N == 1) {
     *reinterpret_cast<uint16_t *>(dst) = (uint16_t)Two<T>::pack(o[0], 0.f);
-    return;
-  }
-  uint32_t p[N / 2 + 1];
+  } else {
+    uint32_t p[N / 2];
 #pragma unroll
-  for (int e = 0; e < N / 2; ++e) p[e] = Two<T>::pack(o[2 * e], o[2 * e + 1]);
-  if constexpr (N == 8)
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(p[0], p[1], p[2], p[3]);
-  else if constexpr (N == 4)
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(p[0], p[1]);
-  else
-    *reinterpret_cast<uint32_t *>(dst) = p[0];
+    for (int e = 0; e < N / 2; ++e) p[e] = Two<T>::pack(o[2 * e], o[2 * e + 1]);
+    if constexpr (N == 8)
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(p[0], p[1], p[2], p[3]);
+    else if constexpr (N == 4)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(p[0], p[1]);
+    else
+      *reinterpret_cast<uint32_t *>(dst) = p[0];
+  }
 }
 
 __device__ __forceinline__ void write_lse(const TreeArgs &a, int s, int h, int r, float m, float l) {
