@@ -447,6 +447,8 @@ class PagedCache:
                  device="cuda"):
         if min(seqs, max_len, pages, hkv, d, page, layers) < 1:
             raise ValueError("sizes must be positive")
+        if dtype not in _HALVES:
+            raise TypeError("dtype must be bf16 or fp16")
         self.page = page
         self.k = torch.zeros(layers, pages, hkv, page, d, dtype=dtype, device=device)
         self.v = torch.zeros_like(self.k)

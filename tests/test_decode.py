@@ -244,6 +244,8 @@ def test_binding_refuses_host_tensors():
             pbs.cache_copy(x, *bad)
     with pytest.raises(ValueError):
         pbs.PagedCache(0, 16, 4, 2, 64, device="cpu")
+    with pytest.raises(TypeError):
+        pbs.PagedCache(1, 16, 4, 2, 64, dtype=torch.float32, device="cpu")
 
 
 def test_rows_of_strided_tensors():

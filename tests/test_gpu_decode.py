@@ -603,7 +603,9 @@ def test_long_context_split_over_every_sm(dev):
 
 
 @pytest.mark.parametrize("tree,hq,hkv,b,most", [(64, 32, 8, 24, 900), (1, 32, 8, 150, 400),
-                                                (20, 16, 8, 40, 3000), (100, 8, 2, 9, 2000)])
+                                                (20, 16, 8, 40, 3000), (100, 8, 2, 9, 2000),
+                                                (1024, 2, 2, 2, 300), (3, 64, 1, 3, 700),
+                                                (5, 1, 1, 70, 90)])
 def test_many_items_in_a_run(tree, hq, hkv, b, most, dev):
     """Batches whose CTAs work through several items each, drafts that span key
     tiles in one after the other: against the formula in fp64 on the GPU, within
@@ -756,6 +758,22 @@ def test_tree_attn_refuses(dev):
     with pytest.raises(pbs.PbsError):
         pbs.tree_attn(**dict(ok, k_pages=t.k[:, :, :12].contiguous(), v_pages=t.v[:, :, :12].contiguous()))
     assert pbs.tree_attn(**dict(ok, q=q[:, :, :0])).shape == (2, 4, 0, 64)
+
+
+@pytest.mark.parametrize("tree", [1, 9, 70])
+def test_nothing_to_do_and_large_pages(tree, dev):
+    """A batch without drafts: allocated rows are 0, given ones stay. Then pages
+    of 256 tokens that end inside tiles and hold several."""
+    start, zero = [300, 0, 255, 1000], [0] * 4
+    t = Tree(dev, FP16, 64, 256, 2, start, [tree] * 4, tree, seed=tree)
+    q = torch.randn(4, 4, tree, 64, device=dev).half()
+    o, lse = pbs.tree_attn(q, t.k, t.v, t.table, i32(start, dev), count=i32(zero, dev), lse=True)
+    assert not o.any() and not lse.any()
+    out = torch.full_like(o, 5)
+    pbs.tree_attn(q, t.k, t.v, t.table, i32(start, dev), count=i32(zero, dev), out=out)
+    assert (out == 5).all()
+    o, lse = pbs.tree_attn(q, t.k, t.v, t.table, i32(start, dev), lse=True)
+    t.check(q, o, lse, chains(tree, start), 1 / 8, FP16)
 
 
 def test_lengths_beyond_the_table_are_reported(dev):
