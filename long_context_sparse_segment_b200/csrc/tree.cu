@@ -80,8 +80,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     bar->abort = 0;
     fence_barrier_init();
   }
-  allow_next();
   __syncthreads();
+  wait_previous();
+  allow_next();  // not before the wait: the next kernel looks at the lengths at once
   Place place;
   if (!find_place<ROWS, kKeys, kMmaThreads>(a, bar->sum, &place)) return;
   // a tile in shared memory: [piece of a page][64-column half][row][128 bytes]
@@ -383,6 +384,7 @@ __global__ void __launch_bounds__(256)
     tree_mask_kernel(const int32_t *__restrict__ parents, uint32_t *mask, int32_t *depth, int tree,
                      int words, int *err) {
   __shared__ int par[kMaxTree];
+  allow_next();
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
   for (int x = threadIdx.x; x < tree; x += 256) {
@@ -478,8 +480,7 @@ cudaError_t run_mma(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs
   constexpr auto kern = tree_mma_kernel<T, D>;
   cudaError_t e = allow_smem<kern>((int)C::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kMmaThreads, C::SMEM, st>>>(mk, mv, a);
-  e = cudaGetLastError();
+  e = launch_behind(kern, dim3(grid), kMmaThreads, C::SMEM, st, mk, mv, a);
   if (e != cudaSuccess) return e;
   return launch_combine<T, D, C::ROWS>(a, grid, st);
 }

@@ -29,6 +29,35 @@ namespace tree {
 
 using namespace tc;
 
+// Programmatic dependent launch. The kernels of a call are launched while the
+// kernel in front of them may still run, set themselves up, and wait for its end
+// before they read or write anything that another kernel knows: 1 to 2 us a call.
+// Every block waits, so that a kernel never ends before the one in front.
+// Allows the kernel launched behind this one to start.
+__device__ __forceinline__ void allow_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Waits until the kernel launched before this one has ended, its writes visible.
+__device__ __forceinline__ void wait_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 constexpr int kMaxTree = 1024;   // 32 mask words a row
 
 struct TreeArgs {
@@ -334,20 +363,10 @@ __device__ __forceinline__ float part_scale(float m, float top) {
 // Joins the parts of the rows that several CTAs worked on. A block takes every
 // gridDim.x-th group of RB rows of one (sequence, KV head): a thread holds 4
 // columns of a row and every PG-th part of it, in order; the PG partial results
-// are joined in shared memory. It is launched while the attention kernel still
-// runs (programmatic dependent launch). Bound by latency: a part is read once,
-// a thread's reads in flight together; most blocks find that nobody shared
-// their items and end.
+// are joined in shared memory. Bound by latency: a part is read once, a thread's
+// reads in flight together; most blocks find that nobody shared their items and
+// end.
 constexpr int kCombineThreads = 512;
-
-// Allows the kernel launched behind this one to start.
-__device__ __forceinline__ void allow_next() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-// Waits until the kernel launched before this one has ended, its writes visible.
-__device__ __forceinline__ void wait_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
 
 struct Part {
   float m, l;
@@ -370,12 +389,13 @@ __global__ void __launch_bounds__(kCombineThreads)
   __shared__ float4 so[kCombineThreads];
   __shared__ float2 sml[PG][RB];
   const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
-  const Seq q = seq_of(a, s);
+  allow_next();
+  const Seq q = seq_of(a, s);  // the attention kernel has not changed it
   const int rows = q.count * a.G, all = a.tree * a.G;  // of the (sequence, KV head)
   const int r = tid % RB, c4 = tid / RB % C4, pg = tid / E;
   // results: neighbouring threads along a row
   const int er = tid / C4, ec = tid % C4 * 4;
-  wait_previous();  // on every path, so that this kernel never ends before the other
+  wait_previous();
   for (int r0 = blockIdx.x * RB; r0 < all; r0 += gridDim.x * RB) {
     if (a.zero_rest && tid < E && r0 + er >= rows && r0 + er < all) {
       const float o[4] = {};
@@ -444,17 +464,11 @@ cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
   const int rb = ceil_div(rows, 4) * heads <= fit ? 4 : 16;
   int64_t gx = ceil_div(rows, rb);
   if (gx * heads > 4 * fit) gx = ceil_div(4 * fit, heads);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)gx, a.hkv, a.seqs);
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return rb == 4 ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, 4>, a, grid)
-                 : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, D, ROWS, 16>, a, grid);
+  const dim3 blocks((unsigned)gx, a.hkv, a.seqs);
+  return rb == 4 ? launch_behind(tree_combine_kernel<T, D, ROWS, 4>, blocks, kCombineThreads, 0,
+                                 st, a, grid)
+                 : launch_behind(tree_combine_kernel<T, D, ROWS, 16>, blocks, kCombineThreads, 0,
+                                 st, a, grid);
 }
 
 }  // namespace tree

@@ -124,10 +124,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh->abort = 0;
     fence_barrier_init();
   }
-  allow_next();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  wait_previous();
+  allow_next();  // not before the wait: the next kernel looks at the lengths at once
   const uint32_t tbase = sh->tmem;
   {
     Place place;
@@ -608,8 +609,7 @@ cudaError_t run(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a,
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  kern<<<grid, kThreads, C::SMEM, st>>>(mk, mv, a);
-  e = cudaGetLastError();
+  e = launch_behind(kern, dim3(grid), kThreads, C::SMEM, st, mk, mv, a);
   if (e != cudaSuccess) return e;
   return launch_combine<T, D, C::ROWS>(a, grid, st);
 }

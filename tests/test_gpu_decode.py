@@ -837,6 +837,33 @@ def test_captured_steps_read_lengths_at_replay(tree, g, dev):
             assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
 
 
+@pytest.mark.parametrize("tree,g", [(1, 4), (40, 2)])
+def test_calls_right_behind_what_they_read(tree, g, dev):
+    """Queries, lengths and rows written by the kernel just in front of each
+    call, results read by the one just behind, over and over on one stream."""
+    t = Tree(dev, BF16, 128, 64, 2, [900, 333], [tree] * 2, tree, junk=False)
+    start = torch.zeros(2, dtype=torch.int32, device=dev)
+    q = torch.zeros(2, 2 * g, tree, 128, dtype=BF16, device=dev)
+    out, sums = torch.empty_like(q), torch.zeros_like(q, dtype=torch.float32)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=dev)
+    draws = [torch.randn(q.shape, device=dev).to(BF16) for _ in range(4)]
+    lens = [i32(x, dev) for x in ([900, 333], [64, 200], [500, 1], [0, 128])]
+    want = []
+    for i in range(4):
+        want.append(pbs.tree_attn(draws[i], t.k, t.v, t.table, lens[i]))
+        torch.cuda.synchronize()
+    for n in range(40):
+        i = n % 4
+        big = torch.ones(1 << 24, device=dev).cumsum(0)  # keeps the stream busy in front
+        start.copy_(lens[i])
+        q.copy_(draws[i])
+        pbs.tree_attn(q, t.k, t.v, t.table, start, out=out, ws=ws)
+        sums += (out.float() - want[i].float()).abs()
+        out.fill_(9)
+        del big
+    assert not sums.any()
+
+
 def test_two_calls_at_once_on_two_streams(dev):
     t = [Tree(dev, BF16, 128, 64, 2, [900, 333], [3, 2], 3, seed=i) for i in range(2)]
     q = [torch.randn(2, 8, 3, 128, device=dev).to(BF16) for _ in range(2)]
