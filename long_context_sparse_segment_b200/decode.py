@@ -22,6 +22,7 @@ _TYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16, torch.float32: _l
 _LAYOUTS = {"half": 0, "pairs": 1}
 _HALVES = (torch.bfloat16, torch.float16)
 _NONE = Rows(None, 0, 0, 0, 0)
+_push, _pop = torch.cuda.nvtx.range_push, torch.cuda.nvtx.range_pop
 _VEC = {torch.bfloat16: 7, torch.float16: 7, torch.float32: 3}  # elements of 16 bytes, less one
 
 
@@ -59,14 +60,17 @@ def _ptr(t):
 def _call(name, dev, *args):
     """One C-ABI call on the current stream of device ``dev`` (its last
     argument), with that device current, inside an NVTX range of its name."""
-    if dev.index != torch.cuda.current_device():
+    at = dev.index
+    if at != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call(name, dev, *args)
-    torch.cuda.nvtx.range_push(name)
+    _push(name)
     try:
-        check(getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
+        status = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(at))
     finally:
-        torch.cuda.nvtx.range_pop()
+        _pop()
+    if status:
+        check(status, name)
 
 
 def _rows(t, name, written=False):
@@ -74,9 +78,12 @@ def _rows(t, name, written=False):
     contiguous, the others multiples of 16 bytes; a tensor that is written may
     not overlap itself."""
     stride, p, odd = t.stride(), t.data_ptr(), _VEC[t.dtype]
-    if not written and len(stride) == 4 and stride[3] == 1 and not (
-            p & 15 or (stride[0] | stride[1] | stride[2]) & odd):
-        return Rows(p, 0, stride[0], stride[1], stride[2])
+    if not written and stride[-1] == 1 and not p & 15:
+        if len(stride) == 4:
+            if not (stride[0] | stride[1] | stride[2]) & odd:
+                return Rows(p, 0, stride[0], stride[1], stride[2])
+        elif not (stride[0] | stride[1] | stride[2] | stride[3]) & odd:
+            return Rows(p, *stride[:4])
     size = t.shape
     if size[-1] > 1 and stride[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
@@ -186,27 +193,27 @@ def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=No
         raise ValueError("inv_freq: 2 * len must be a multiple of 16 and at most d")
     each = isinstance(pos, torch.Tensor) and pos.dim() == 1
     _ints(pos, "pos", (n,) if each else (b, n), dev)
-    outs, rows = [], []
-    for x, y, h, nm in ((q, q_out, hq, "q"), (k, k_out, hkv, "k")):
-        if x is None:
-            rows += (_NONE, _NONE)
-            continue
-        if y is None:
-            new = _fresh(x)
-            to = Rows(new.data_ptr(), 0, h * n * d, n * d, d)
-        else:
-            new = y
-            _on(y, nm + "_out", dev)
-            if y.shape != x.shape or y.dtype is not t:
-                raise ValueError(f"{nm}_out must have the shape and type of its input")
-            to = _rows(y, nm + "_out", True) if y.numel() else _NONE
-        outs.append(new)
-        rows += (_rows(x, nm) if x.numel() else _NONE, to)
+    q_out, q_to = _rope_out(q, q_out, "q_out", hq, n, d)
+    k_from = k_to = _NONE
+    if k is not None:
+        k_out, k_to = _rope_out(k, k_out, "k_out", hkv, n, d)
+        k_from = _rows(k, "k") if hkv else _NONE
     if b and n and hq + hkv:
-        _call("pbs_rope", dev, rows[0], rows[1], hq, rows[2], rows[3], hkv, pos.data_ptr(),
-              0 if each else n, inv_freq.data_ptr() if rot else None, gain, b, n, d, rot, order,
-              1 if transpose else 0, kind)
-    return outs[0] if k is None else tuple(outs)
+        _call("pbs_rope", dev, _rows(q, "q") if hq else _NONE, q_to, hq, k_from, k_to, hkv,
+              pos.data_ptr(), 0 if each else n, inv_freq.data_ptr() if rot else None, gain, b, n,
+              d, rot, order, 1 if transpose else 0, kind)
+    return q_out if k is None else (q_out, k_out)
+
+
+def _rope_out(x, y, name, h, n, d):
+    """The tensor that takes x's result, and its rows."""
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        return y, Rows(y.data_ptr(), 0, h * n * d, n * d, d)
+    _on(y, name, x.device)
+    if y.shape != x.shape or y.dtype is not x.dtype:
+        raise ValueError(f"{name} must have the shape and type of its input")
+    return y, _rows(y, name, True) if y.numel() else _NONE
 
 
 # ------------------------------------------------------------------ the cache
@@ -214,28 +221,35 @@ def _pools(k_pages, v_pages, table=None):
     """The pools [layers, pages, hkv, page, d] (or one layer's, 4-D)."""
     _on(k_pages, "k_pages")
     dev, size = k_pages.device, k_pages.shape
+    n = len(size)
     _on(v_pages, "v_pages", dev)
-    if len(size) not in (4, 5) or k_pages.element_size() != 2:
+    if n < 4 or n > 5 or k_pages.element_size() != 2:
         raise ValueError("k_pages must be [layers, pages, hkv, page, d] (or 4-D) of a 16-bit type")
     if v_pages.shape != size or v_pages.dtype is not k_pages.dtype:
         raise ValueError("v_pages must have the shape and type of k_pages")
     if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages and v_pages must be contiguous")
-    if 0 in size:
+    if not k_pages.numel():
         raise ValueError("k_pages is empty")
-    if size[-1] % 8:
+    layers, pages, hkv, page, d = size if n == 5 else (1, *size)
+    if d % 8:
         raise ValueError("the head dimension must be a multiple of 8")
-    seqs, width = (0, 1) if table is None else _table(table, dev)
-    return Cache(*(size if len(size) == 5 else (1, *size)), seqs, width)
+    if table is None:
+        return Cache(layers, pages, hkv, page, d, 0, 1)
+    seqs, width = _table(table, dev)
+    return Cache(layers, pages, hkv, page, d, seqs, width)
 
 
 def _table(table, device=None):
-    _on(table, "table", device)
-    size = table.shape
-    if len(size) != 2 or size[1] < 1:
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        _on(table, "table", device)
         raise ValueError("table must be [seqs, width]")
-    _ints(table, "table", size, table.device)
-    return size
+    size = table.shape
+    _ints(table, "table", size, table.device if device is None else device)
+    seqs, width = size
+    if width < 1:
+        raise ValueError("table must have a column")
+    return seqs, width
 
 
 def _books(table, refs, lens, page):
@@ -420,7 +434,7 @@ def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.
             raise ValueError("out must not be q")
     l = None
     if lse:
-        l = out.new_empty(size[:3], dtype=torch.float32)
+        l = out.new_empty((seqs, hq, tree), dtype=torch.float32)
         if count is not None and not zero:
             l.zero_()
     if not (seqs and tree):
