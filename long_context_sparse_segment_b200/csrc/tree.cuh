@@ -33,6 +33,7 @@ using namespace tc;
 // kernel in front of them may still run, set themselves up, and wait for its end
 // before they read or write anything that another kernel knows: 1 to 2 us a call.
 // Every block waits, so that a kernel never ends before the one in front.
+
 // Allows the kernel launched behind this one to start.
 __device__ __forceinline__ void allow_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -58,7 +59,7 @@ cudaError_t launch_behind(void (*kern)(P...), dim3 grid, int threads, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-constexpr int kMaxTree = 1024;   // 32 mask words a row
+constexpr int kMaxTree = 1024;  // 32 mask words a row
 
 struct TreeArgs {
   pbs_rows q;
@@ -274,7 +275,8 @@ struct Two<__half> {
   static constexpr uint32_t kExp = 0x7c00u;
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
         "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));

@@ -40,7 +40,7 @@ constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168, kCtrlRegs = 56, kSoftmaxRegs = 224;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split");
 constexpr float kRescaleLog2 = 8.f;  // the running maximum moves by more than 2^8 or not at all
-constexpr int kBadSlots = 8;         // segments in flight, at most kVS + 2
+constexpr int kBadSlots = 8;         // segments in flight: at most VS + 2
 
 template <int D, bool PAIR>
 struct Cfg {
