@@ -453,7 +453,8 @@ typedef enum { PBS_BF16 = 0, PBS_FP16 = 1, PBS_FP32 = 2 } pbs_dtype;
  * turns), so it stays right at any int32 position; sums are fp32 and each
  * element is rounded once.
  *
- *   q, q_out  [batch, hq, n, d]  (layer stride unused); y may be x itself
+ *   q, q_out  [batch, hq, n, d]  (layer stride unused); q_out may be q and
+ *             k_out k, rows and all, and no output overlaps anything else
  *   k, k_out  [batch, hkv, n, d] or k.p == NULL with hkv == 0
  *   pos       int32, pos[b * pos_batch + i] (pos_batch 0: one row for all)
  *   inv_freq  [rot/2] fp64, radians per position
@@ -512,7 +513,8 @@ pbs_status pbs_cache_reserve(int32_t *table, int32_t *refs, const int32_t *lens,
 /*
  * pbs_cache_append - rows i < count[s] (all n when count is NULL) of k, v
  * [layers, seqs, hkv, n, d] written at tokens start[s] + i. The pages must
- * be reserved. No other row of the pools is touched.
+ * be reserved, k and v lie outside the pools, the pools apart. No other row of
+ * the pools is touched.
  */
 pbs_status pbs_cache_append(pbs_rows k, pbs_rows v, int n, void *k_pages, void *v_pages,
                             const int32_t *table, const int32_t *start, const int32_t *count,

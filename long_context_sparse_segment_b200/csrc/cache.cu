@@ -527,7 +527,7 @@ pbs_status pbs_cache_append(pbs_rows k, pbs_rows v, int n, void *k_pages, void *
   if (!cache_ok(c) || n < 0) return PBS_ERR_INVALID_ARG;
   if (c.seqs == 0 || n == 0) return PBS_OK;
   if (!rows_ok(k, 2) || !rows_ok(v, 2) || !pool_ok(k_pages) || !pool_ok(v_pages) ||
-      !ints_ok(table) || !ints_ok(start) || (count && !ints_ok(count)))
+      k_pages == v_pages || !ints_ok(table) || !ints_ok(start) || (count && !ints_ok(count)))
     return PBS_ERR_INVALID_ARG;
   const int64_t total = (int64_t)c.layers * c.seqs * c.hkv * n * (c.d / 8);
   const int64_t blocks = ceil_div(total, 256), most = 148 * 32;
@@ -612,8 +612,9 @@ pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,
   if (!cache_ok(c) || tree < 0) return PBS_ERR_INVALID_ARG;
   if (c.seqs > 65535) return PBS_ERR_UNSUPPORTED;
   if (c.seqs == 0 || tree == 0) return PBS_OK;
-  if (!pool_ok(k_pages) || !pool_ok(v_pages) || !ints_ok(table) || !ints_ok(start) ||
-      !ints_ok(path) || (count && !ints_ok(count)) || (lens && !ints_ok(lens)))
+  // one pool for both would be moved twice at once
+  if (!pool_ok(k_pages) || !pool_ok(v_pages) || k_pages == v_pages || !ints_ok(table) ||
+      !ints_ok(start) || !ints_ok(path) || (count && !ints_ok(count)) || (lens && !ints_ok(lens)))
     return PBS_ERR_INVALID_ARG;
   const int col_blocks = (int)ceil_div((int64_t)c.hkv * (c.d / 8), kAcceptThreads);
   const int64_t gx = 2LL * c.layers * col_blocks;

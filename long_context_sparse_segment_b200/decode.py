@@ -99,6 +99,23 @@ def _rows(t, name, written=False):
     return Rows(p, step[0] if len(step) == 4 else 0, *step[-3:])
 
 
+def _span(t):
+    """The bytes from a tensor's first element to behind its last."""
+    last = sum(st * (n - 1) for st, n in zip(t.stride(), t.shape))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _apart(out, name, *others):
+    """An output that a call was given may not reach into its inputs."""
+    if out.numel():
+        a, b = _span(out)
+        for x in others:
+            if x.numel():
+                c, d = _span(x)
+                if a < d and c < b:
+                    raise ValueError(f"{name} overlaps an input")
+
+
 def rope_freqs(rot, base=10000.0, scaling=None, device=None):
     """(inv_freq [rot/2] fp64, gain) for ``rope``: inv_freq[i] = base^(-2i/rot)
     radians per position, scaled for contexts longer than a model was trained
@@ -163,7 +180,8 @@ def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=No
     16-byte-aligned rows (slices of one projection). pos is int32 [b, n] or
     [n]; the first 2 * len(inv_freq) elements of each head turn. ``transpose``
     turns back: the gradients of q and k from those of the results. Returns
-    (q', k'), or q' alone without k. q_out, k_out may be q and k themselves."""
+    (q', k'), or q' alone without k. q_out may be q itself and k_out k, and they
+    overlap nothing else."""
     _on(q, "q")
     dev, t, size = q.device, q.dtype, q.shape
     kind, order = _TYPES.get(t), _LAYOUTS.get(layout)
@@ -213,6 +231,8 @@ def _rope_out(x, y, name, h, n, d):
     _on(y, name, x.device)
     if y.shape != x.shape or y.dtype is not x.dtype:
         raise ValueError(f"{name} must have the shape and type of its input")
+    if y.data_ptr() != x.data_ptr() or y.stride() != x.stride():
+        _apart(y, name, x)
     return y, _rows(y, name, True) if y.numel() else _NONE
 
 
@@ -430,8 +450,7 @@ def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.
         _on(out, "out", dev)
         if out.shape != size or out.dtype is not t or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape and type")
-        if out.data_ptr() == q.data_ptr() and out.numel():
-            raise ValueError("out must not be q")
+        _apart(out, "out", q, k_pages, v_pages)
     l = None
     if lse:
         l = out.new_empty((seqs, hq, tree), dtype=torch.float32)

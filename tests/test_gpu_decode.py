@@ -124,7 +124,8 @@ def test_rope_refuses(dev):
                 lambda: pbs.rope(q, None, pos, f, layout="x"), lambda: pbs.rope(q[0], None, pos, f),
                 lambda: pbs.rope(q.double(), None, pos, f), lambda: pbs.rope(q[..., ::2], None, pos, f[:16]),
                 lambda: pbs.rope(q, None, pos, f, k_out=q), lambda: pbs.rope(q, None, pos, f.cpu()),
-                lambda: pbs.rope(q, None, pos, f, q_out=q[:1].expand(2, 4, 3, 64))):
+                lambda: pbs.rope(q, None, pos, f, q_out=q[:1].expand(2, 4, 3, 64)),
+                lambda: pbs.rope(q[:1], None, pos[:1], f, q_out=q.view(-1)[64:64 + 768].view(1, 4, 3, 64))):
         with pytest.raises((ValueError, TypeError)):
             bad()
     assert pbs.rope(q[:0], None, pos[:0], f).shape == (0, 4, 3, 64)
@@ -326,6 +327,10 @@ def test_append_and_accept_refuse_pages_they_do_not_have(dev):
     k0[0, 0, 15], v0[0, 0, 15] = bits(new)[0, 0, 0], bits(new)[0, 0, 0]
     k0[2, 0, 15], v0[2, 0, 15] = bits(new)[2, 0, 0], bits(new)[2, 0, 0]
     assert torch.equal(bits(k), k0) and torch.equal(bits(v), v0)
+    for call in (lambda: pbs.cache_append(new, new, k, k, table, i32([0, 0, 0], dev)),
+                 lambda: pbs.cache_accept(k, k, table, i32([0, 0, 0], dev), i32([[0]] * 3, dev))):
+        with pytest.raises(pbs.PbsError):  # one pool for both
+            call()
     lens = i32([7, 8, 9], dev)
     for start, path in (([14, 0, 31], [[1, 2], [0, 1], [1, 2]]),      # pages missing
                         ([0, 0, -1], [[1, 1], [1, 0], [0, 1]]),       # does not ascend; start < 0
@@ -752,6 +757,7 @@ def test_tree_attn_refuses(dev):
                 dict(table=t.table.long()), dict(table=t.table[:, ::2]), dict(start=start[:1]),
                 dict(mask=torch.zeros(2, 2, 2, dtype=torch.int32, device=dev)),
                 dict(count=start.long()), dict(out=q), dict(out=q.transpose(1, 2)),
+                dict(out=t.k.view(-1)[64:64 + q.numel()].view(q.shape)),
                 dict(start=start.cpu()), dict(k_pages=t.k.transpose(1, 2), v_pages=t.v.transpose(1, 2))):
         with pytest.raises((ValueError, TypeError)):
             pbs.tree_attn(**dict(ok, **bad))
