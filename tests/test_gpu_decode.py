@@ -870,6 +870,42 @@ def test_calls_right_behind_what_they_read(tree, g, dev):
     assert not sums.any()
 
 
+@pytest.mark.parametrize("tree,g", [(1, 4), (40, 2)])
+def test_captured_behind_copies_and_joined_streams(tree, g, dev):
+    """A graph in which the call stands behind a copy, behind a kernel of another
+    stream and behind both, and two calls run side by side."""
+    t = Tree(dev, BF16, 128, 64, 2, [900, 333], [tree] * 2, tree, junk=False)
+    src = [torch.randn(2, 2 * g, tree, 128, device=dev).to(BF16) for _ in range(2)]
+    lens = i32(t.start, dev)
+    want = [pbs.tree_attn(x, t.k, t.v, t.table, lens) for x in src]
+    q = [torch.zeros_like(x) for x in src]
+    start = torch.zeros_like(lens)
+    side, graph = torch.cuda.Stream(dev), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            start.copy_(lens)
+            q[1].copy_(src[1])
+        q[0].copy_(src[0])
+        main.wait_stream(side)
+        a = pbs.tree_attn(q[0], t.k, t.v, t.table, start)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            b = pbs.tree_attn(q[1], t.k, t.v, t.table, start)
+        c = pbs.tree_attn(a * 0 + q[0], t.k, t.v, t.table, start)
+        main.wait_stream(side)
+        d = pbs.tree_attn(q[1] + b * 0, t.k, t.v, t.table, start)
+    for _ in range(3):
+        for x in (start, *q):
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, i in ((a, 0), (b, 1), (c, 0), (d, 1)):
+            assert torch.equal(got, want[i])
+
+
 def test_two_calls_at_once_on_two_streams(dev):
     t = [Tree(dev, BF16, 128, 64, 2, [900, 333], [3, 2], 3, seed=i) for i in range(2)]
     q = [torch.randn(2, 8, 3, 128, device=dev).to(BF16) for _ in range(2)]
