@@ -304,7 +304,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             Two<T>::mma(o[2 * n + y], p, b[y >> 1][2 * (y & 1)], b[y >> 1][2 * (y & 1) + 1]);
         }
       }
-      warp_arrive(&bar->empty[st], lane);
+      // not after a wait ran out: the producer would fill a stage whose barrier
+      // still expects its last bytes
+      if (!failed) warp_arrive(&bar->empty[st], lane);
     }
     // ------------------------------------------------ join the eight warps
     bad = __any_sync(0xffffffffu, bad);

@@ -666,6 +666,23 @@ def test_waits_are_bounded(tree, g, dev, monkeypatch):
     assert torch.equal(call(), good)
 
 
+@pytest.mark.parametrize("d,seqs,hkv,tokens", [(64, 1, 8, 130), (128, 64, 8, 130), (128, 2, 8, 9000),
+                                               (64, 2, 8, 9000)])
+def test_waits_end_in_long_runs(d, seqs, hkv, tokens, dev, monkeypatch):
+    """The same where a CTA has more tiles, and more items, than its ring holds."""
+    t = Tree(dev, BF16, d, 64, hkv, [tokens] * seqs, [1] * seqs, 1, junk=False)
+    q = torch.randn(seqs, 4 * hkv, 1, d, device=dev).to(BF16)
+    call = lambda: pbs.tree_attn(q, t.k, t.v, t.table, i32(t.start, dev))
+    good = call()
+    assert pbs.device_status() == 0
+    monkeypatch.setenv("PBS_FAULT_INJECT", "tree")
+    call()
+    code, where = pbs.device_status(detail=True)
+    monkeypatch.delenv("PBS_FAULT_INJECT")
+    assert code == _lib.ERR_TIMEOUT and where > 0
+    assert torch.equal(call(), good)
+
+
 def test_pools_beyond_32_bits(dev):
     """Pools of 4.5 GB each: copies, appends, accepts and attention at pages
     whose offsets pass 2^31 elements and 2^32 bytes."""
