@@ -9,9 +9,12 @@
 // the cache.
 //
 // This kernel: up to 16 rows an item, warp MMA. Eight warps take tiles of 64
-// keys, four warps a tile (16 keys each) and the two halves in turn, each
-// with its own maximum, sum and output, joined when the item ends; a ninth
-// warp brings the tiles by TMA, page by page, into a ring. A unit keeps a warp
+// keys, four warps a tile (16 keys each), each with its own maximum, sum and
+// output, joined when the item ends; one warp more brings the tiles by TMA,
+// page by page, into a ring. The eight are one CTA, whose halves take the tiles
+// of an item in turn, or two CTAs an SM with half the ring each, so that one
+// item's beginning and end go beside the other CTA's tiles (mma_warps has the
+// rule, with both sides). A unit keeps a warp
 // busy for 1,450 cycles, two warps a scheduler, while its 32 KB (d = 128) take
 // 1,450 to arrive at the copy rate: the tensor core of tcgen05 would have 4 to
 // 16 of its 128 rows to do. Measured: a new token of each of 48 sequences of
@@ -31,36 +34,37 @@ using namespace tree;
 
 // ------------------------------------------------------------- warp-MMA kernel
 constexpr int kKeys = 64;       // keys of a unit
-constexpr int kConsumers = 8;   // warps
-constexpr int kMmaThreads = 32 * (kConsumers + 1);
 
-template <int D>
+template <int D, int W>  // W: consumer warps
 struct MmaCfg {
   static constexpr int ROWS = 16;
   static constexpr uint32_t KV = kKeys * D * 2;   // bytes of a K or V tile
   // 192 KB in flight an SM (128 KB: 6 % slower on a ragged batch, 64 KB: 30 %);
-  // even: a stage stays with one half
-  static constexpr int ST = D == 128 ? 6 : 12;
-  static constexpr int RJ = 4;                    // rows joined at a time
+  // even with two halves: a stage stays with one of them
+  static constexpr int ST = (D == 128 ? 6 : 12) * W / 8;
+  static constexpr int CTAS = 8 / W;              // an SM
+  static constexpr int THREADS = 32 * (W + 1);
+  static constexpr int RJ = W / 2;                // rows joined at a time
   static constexpr int PAD = 4;                   // floats behind a joined row
-  static constexpr size_t JOIN = (size_t)kConsumers * RJ * (D + PAD) * 4;
+  static constexpr size_t JOIN = (size_t)W * RJ * (D + PAD) * 4;
   struct Bars {
     uint64_t full[ST], empty[ST], q_full[2], q_empty[2];
     int abort;
-    int bad[kConsumers];
+    int bad[W];
     Segment g[2];
-    float2 ml[kConsumers][ROWS];
-    int sum[kConsumers + 1];
+    float2 ml[W][ROWS];
+    int sum[W + 1];
   };
   static constexpr size_t SMEM = 1024 + 2 * KV * ST + 2 * ROWS * D * 2 + JOIN + sizeof(Bars);
+  // 228 KB an SM, of which every CTA takes 1 KB more than it asks for
+  static_assert((SMEM + 1024) * CTAS <= 233472, "shared memory");
 };
-static_assert(MmaCfg<128>::SMEM <= 232448 && MmaCfg<64>::SMEM <= 232448, "shared memory");
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kMmaThreads, 1)
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(MmaCfg<D, W>::THREADS, MmaCfg<D, W>::CTAS)
     tree_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a) {
-  using C = MmaCfg<D>;
+  using C = MmaCfg<D, W>;
   constexpr int ST = C::ST, ROWS = C::ROWS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>(
@@ -75,7 +79,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     for (int i = 0; i < ST; ++i) mbar_init(&bar->full[i], 1), mbar_init(&bar->empty[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->q_full[i], 33);  // each lane's copies, and the segment
-      mbar_init(&bar->q_empty[i], kConsumers);
+      mbar_init(&bar->q_empty[i], W);
     }
     bar->abort = 0;
     fence_barrier_init();
@@ -84,11 +88,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   wait_previous();
   allow_next();  // not before the wait: the next kernel looks at the lengths at once
   Place place;
-  if (!find_place<ROWS, kKeys, kMmaThreads>(a, bar->sum, &place)) return;
+  if (!find_place<ROWS, kKeys, C::THREADS>(a, bar->sum, &place)) return;
   // a tile in shared memory: [piece of a page][64-column half][row][128 bytes]
   const int box = min(a.page, kKeys);
 
-  if (warp == kConsumers) {
+  if (warp == W) {
     // ------------------------------------------------------------- producer
     // Finds the segments, brings each one's Q rows (a segment ahead of the
     // consumers, as the ring allows) and its units: up to 4 pieces of pages,
@@ -167,18 +171,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   // --------------------------------------------------------------- consumers
   const int half_id = warp >> 2, key16 = (warp & 3) * 16;
   const int gr = lane >> 2, qc = (lane & 3) * 2;
-  // The eight warps meet in named barriers (a bounded mbarrier wait instead costs
+  // The consumers meet in named barriers (a bounded mbarrier wait instead costs
   // 0.2 us each, up to eight an item). So a warp whose wait ran out goes on to
   // every barrier of the segment, and all leave together at the next one.
-  auto sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+  auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory"); };
   bool failed = false;
   auto agree = [&]() {
     int any;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 256, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        "bar.red.or.pred q, 1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
-        : "r"((int)failed)
+        : "r"((int)failed), "n"(32 * W)
         : "memory");
     failed = any != 0;
   };
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     bool bad = false;
     for (int k = g.k0; k < g.k1; ++k, ++it) {
-      if ((it & 1) != half_id) continue;
+      if (W == 8 && (it & 1) != half_id) continue;
       const int st = it % ST;
       if (!failed && !mbar_wait_warp(&bar->full[st], (it / ST) & 1, abort, a.err, 41))
         failed = true;
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       // still expects its last bytes
       if (!failed) warp_arrive(&bar->empty[st], lane);
     }
-    // ------------------------------------------------ join the eight warps
+    // ------------------------------------------------ join the warps
     bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -317,11 +321,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     const int slot = 2 * blockIdx.x + (seg > 0);
     if (tid == 0) tell_item(a, g, place.run, slot);
-    constexpr int RJ = C::RJ, N = D * RJ / (32 * kConsumers);  // columns a thread joins
+    constexpr int RJ = C::RJ, N = D * RJ / (32 * W);  // columns a thread joins
     auto any_bad = [&]() {
       int x = 0;
 #pragma unroll
-      for (int w = 0; w < kConsumers; ++w) x |= bar->bad[w];
+      for (int w = 0; w < W; ++w) x |= bar->bad[w];
       return x;
     };
     for (int r0 = 0; r0 < rows; r0 += RJ) {
@@ -345,12 +349,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       if (r < rows) {
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, bar->ml[w][r].x);
+        for (int w = 0; w < W; ++w) top = fmaxf(top, bar->ml[w][r].x);
         float sum = 0.f, acc[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) acc[e] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kConsumers; ++w) {
+        for (int w = 0; w < W; ++w) {
           const float2 ml = bar->ml[w][r];
           const float f = part_scale(ml.x, top);
           const float *src = join + (w * RJ + r - r0) * (D + C::PAD) + col;
@@ -446,8 +450,8 @@ bool tree_supported(int hq, int tree, const pbs_cache &c) {
 //   rows, sequences x tokens    16 by MMA   128 alone   256 in pairs
 //   4    8 x 16K                     91.9        89.4          -
 //   16   8 x 16K                     96.2        90.2          -
-//   4    64 x 1000                   53.8        75.4          -
-//   16   64 x 1000                   65.7        75.6          -
+//   4    64 x 1000                   54.4        75.4          -
+//   16   64 x 1000                   60.7        75.6          -
 //   4    1 x 8K                      17.2        20.0          -
 //   32   8 x 16K                        -        94.1      107.5
 //   128  8 x 16K                        -       105.6      114.8
@@ -459,12 +463,45 @@ int row_tile(int hq, int tree, const pbs_cache &c) {
   return rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
 }
 
+// Consumer warps of a CTA of the warp-MMA kernel: 8, or 4 in each of two CTAs an
+// SM. Two CTAs hide the 3 to 5 us that an item's beginning and end cost, and
+// have two warps to issue the copies, where 16-token pages of d = 64 keep one
+// busy; their twice as many runs leave more parts to join, and a long item reads
+// a little slower. Us a call (4 rows, 8 KV heads, captured):
+//   d, page   sequences x tokens    8 warps   2 x 4
+//   128, 64   2000 x 50               428.2   274.1
+//   128, 64   512 x 200               156.8   118.3
+//   128, 64   32 x 300                 21.9    18.3
+//   128, 64   64 x 1000                54.4    54.2
+//   128, 64   32 x 8000               171.3   171.8
+//   128, 64   64 x 4000               172.7   174.5
+//   128, 16   64 x 4000               167.8   172.5
+//   128, 64   1 x 32000                34.7    36.0
+//   64, 64    256 x 1000              118.4   100.4
+//   64, 64    32 x 8000                96.2    94.8
+//   64, 16    32 x 8000               142.3    89.5
+//   64, 16    1 x 32000                26.2    21.9
+//   64, 64    1 x 32000                22.3    22.5
+//   128, 64   1 x 131072, 1 KV head    32.5    46.0
+// The lengths are on the device; the host knows the items (a KV head of a
+// sequence) and the most tokens that a table row can name.
+int mma_warps(const pbs_cache &c) {
+  const int64_t items = (int64_t)c.seqs * c.hkv, most = (int64_t)c.width * c.page;
+  if (c.d == 64) return items >= 8 ? 4 : 8;
+  return items >= 512 || (items >= 128 && most <= 1024) ? 4 : 8;
+}
+
+// CTAs of the attention kernel.
+int ctas(int rows, const pbs_cache &c) {
+  return sm_count_cached() * (rows == 16 ? 8 / mma_warps(c) : 1);
+}
+
 struct Parts {
   size_t o, ml, items, bad, bytes;
   int tiles;
 };
 Parts parts(int rows, int hq, int tree, const pbs_cache &c) {
-  const size_t slots = 2 * (size_t)sm_count_cached();
+  const size_t slots = 2 * (size_t)ctas(rows, c);
   Parts p;
   p.tiles = (int)ceil_div((int64_t)(hq / c.hkv) * tree, rows);
   p.o = 0;
@@ -475,16 +512,26 @@ Parts parts(int rows, int hq, int tree, const pbs_cache &c) {
   return p;
 }
 
-template <typename T, int D>
+template <typename T, int D, int W>
 cudaError_t run_mma(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int grid,
                     cudaStream_t st) {
-  using C = MmaCfg<D>;
-  constexpr auto kern = tree_mma_kernel<T, D>;
+  using C = MmaCfg<D, W>;
+  constexpr auto kern = tree_mma_kernel<T, D, W>;
   cudaError_t e = allow_smem<kern>((int)C::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_behind(kern, dim3(grid), kMmaThreads, C::SMEM, st, mk, mv, a);
+  e = launch_behind(kern, dim3(grid), C::THREADS, C::SMEM, st, mk, mv, a);
   if (e != cudaSuccess) return e;
   return launch_combine<T, D, C::ROWS>(a, grid, st);
+}
+
+template <typename T>
+cudaError_t run_mma(const CUtensorMap &mk, const CUtensorMap &mv, const TreeArgs &a, int d,
+                    int warps, int grid, cudaStream_t st) {
+  if (d == 64)
+    return warps == 4 ? run_mma<T, 64, 4>(mk, mv, a, grid, st)
+                      : run_mma<T, 64, 8>(mk, mv, a, grid, st);
+  return warps == 4 ? run_mma<T, 128, 4>(mk, mv, a, grid, st)
+                    : run_mma<T, 128, 8>(mk, mv, a, grid, st);
 }
 
 }  // namespace
@@ -555,17 +602,14 @@ pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
   if (!make(&mk, k_pages, all, c.d, box) || !make(&mv, v_pages, all, c.d, box))
     return PBS_ERR_CUDA;
   cudaStream_t cs = (cudaStream_t)st;
-  const int grid = sm_count_cached();
+  const int grid = ctas(rows, c);
   const bool bf16 = dtype == PBS_BF16;
   cudaError_t e;
   if (rows > 16)
     e = launch_tree_tc(mk, mv, a, c.d, rows, bf16, grid, cs);
-  else if (c.d == 64)
-    e = bf16 ? run_mma<__nv_bfloat16, 64>(mk, mv, a, grid, cs)
-             : run_mma<__half, 64>(mk, mv, a, grid, cs);
   else
-    e = bf16 ? run_mma<__nv_bfloat16, 128>(mk, mv, a, grid, cs)
-             : run_mma<__half, 128>(mk, mv, a, grid, cs);
+    e = bf16 ? run_mma<__nv_bfloat16>(mk, mv, a, c.d, mma_warps(c), grid, cs)
+             : run_mma<__half>(mk, mv, a, c.d, mma_warps(c), grid, cs);
   return e == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
 }
 

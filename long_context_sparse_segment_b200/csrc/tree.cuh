@@ -2,9 +2,9 @@
 // is cut into runs, the types, and the kernel that joins the parts.
 //
 // Work. The key tiles of all items (sequence, KV head, tile of rows) form
-// one line of units, cut into equal runs, one per CTA (one CTA per SM): a
-// ragged batch and a single long sequence load every SM alike, and the
-// lengths are read on the device. A run that holds all of an item's units
+// one line of units, cut into equal runs, one per CTA (one CTA per SM, or two
+// of half the size): a ragged batch and a single long sequence load every SM
+// alike, and the lengths are read on the device. A run that holds all of an item's units
 // writes its rows; an item cut by a run's end leaves its running maximum,
 // sum and output (fp32) in the workspace, at most two per CTA, and the
 // combining kernel joins them in unit order, so results do not depend on

@@ -666,12 +666,52 @@ def test_waits_are_bounded(tree, g, dev, monkeypatch):
     assert torch.equal(call(), good)
 
 
+@pytest.mark.parametrize("d,seqs,hkv,g,tree,most,page", [
+    (128, 65, 8, 4, 1, 200, 64), (128, 520, 1, 5, 3, 70, 16), (128, 33, 4, 1, 16, 500, 128),
+    (128, 128, 1, 16, 1, 1023, 32), (64, 9, 1, 3, 5, 2500, 16), (64, 70, 2, 1, 12, 300, 64),
+    (64, 4, 2, 16, 1, 5000, 256), (64, 300, 3, 2, 2, 40, 16)])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_many_short_sequences(d, seqs, hkv, g, tree, most, page, dtype, dev):
+    """Few rows and many items, ragged: empty sequences, drafts across tiles, and
+    in every third sequence NaN in a draft that only its own row sees."""
+    r = random.Random(seqs)
+    start = [r.choice([0, r.randint(0, 70), r.randint(0, most)]) for _ in range(seqs)]
+    start[0] = most
+    count = [r.randint(0, tree) if tree > 1 else 1 for _ in range(seqs)]
+    t = Tree(dev, dtype, d, page, hkv, start, count, tree, seqs)
+    see, wild = [], set()
+    for s in range(seqs):
+        x = np.tril(np.ones((tree, tree), dtype=bool))
+        if s % 3 == 0 and count[s] > 1:
+            j = count[s] - 1
+            n = start[s] + j
+            p, o = int(t.table[s, n // page]), n % page
+            t.v[p, :, o] = float("nan")
+            t.rows[s][1][:, n] = float("nan")
+            x[:, j] = False
+            x[j, j] = True
+            wild |= {(s, h) for h in range(hkv)}
+        see.append(x)
+    q = (2 * torch.randn(seqs, hkv * g, tree, d, generator=torch.Generator().manual_seed(3)))
+    q = q.to(dtype).to(dev)
+    call = lambda: pbs.tree_attn(q, t.k, t.v, t.table, i32(start, dev), pack_mask(see, tree, dev),
+                                 i32(count, dev), lse=True)
+    o, lse = call()
+    assert pbs.device_status() == 0
+    t.check(q, o, lse, see, 1 / math.sqrt(d), dtype, wild=wild)
+    for s in range(seqs):
+        assert not o[s, :, count[s]:].any()
+    again = call()  # the same on every run
+    assert torch.equal(bits(o), bits(again[0])) and torch.equal(bits(lse), bits(again[1]))
+
+
 @pytest.mark.parametrize("d,seqs,hkv,tokens", [(64, 1, 8, 130), (128, 64, 8, 130), (128, 2, 8, 9000),
                                                (64, 2, 8, 9000)])
-def test_waits_end_in_long_runs(d, seqs, hkv, tokens, dev, monkeypatch):
+@pytest.mark.parametrize("tree", [1, 9, 64])
+def test_waits_end_in_long_runs(tree, d, seqs, hkv, tokens, dev, monkeypatch):
     """The same where a CTA has more tiles, and more items, than its ring holds."""
-    t = Tree(dev, BF16, d, 64, hkv, [tokens] * seqs, [1] * seqs, 1, junk=False)
-    q = torch.randn(seqs, 4 * hkv, 1, d, device=dev).to(BF16)
+    t = Tree(dev, BF16, d, 64, hkv, [tokens] * seqs, [tree] * seqs, tree, junk=False)
+    q = torch.randn(seqs, 4 * hkv, tree, d, device=dev).to(BF16)
     call = lambda: pbs.tree_attn(q, t.k, t.v, t.table, i32(t.start, dev))
     good = call()
     assert pbs.device_status() == 0
