@@ -44,7 +44,7 @@ struct MmaCfg {
   static constexpr int ST = (D == 128 ? 6 : 12) * W / 8;
   static constexpr int CTAS = 8 / W;              // an SM
   static constexpr int THREADS = 32 * (W + 1);
-  static constexpr int RJ = W / 2;                // rows joined at a time
+  static constexpr int RJ = 4;                    // rows joined at a time
   static constexpr int PAD = 4;                   // floats behind a joined row
   static constexpr size_t JOIN = (size_t)W * RJ * (D + PAD) * 4;
   struct Bars {
@@ -55,7 +55,7 @@ struct MmaCfg {
     float2 ml[W][ROWS];
     int sum[W + 1];
   };
-  static constexpr size_t SMEM = 1024 + 2 * KV * ST + 2 * ROWS * D * 2 + JOIN + sizeof(Bars);
+  static constexpr size_t SMEM = 2 * KV * ST + 2 * ROWS * D * 2 + JOIN + sizeof(Bars);
   // 228 KB an SM, of which every CTA takes 1 KB more than it asks for
   static_assert((SMEM + 1024) * CTAS <= 233472, "shared memory");
 };
@@ -66,15 +66,17 @@ __global__ void __launch_bounds__(MmaCfg<D, W>::THREADS, MmaCfg<D, W>::CTAS)
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a) {
   using C = MmaCfg<D, W>;
   constexpr int ST = C::ST, ROWS = C::ROWS;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *base = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t *ring = base;                          // [ST][K tile, V tile]
+  extern __shared__ __align__(1024) uint8_t smem_raw[];  // the swizzle's alignment
+  uint8_t *ring = smem_raw;                          // [ST][K tile, V tile]
   T *sQ = reinterpret_cast<T *>(ring + 2 * C::KV * ST);  // [2][ROWS][D]
   float *join = reinterpret_cast<float *>(sQ + 2 * ROWS * D);
   auto *bar = reinterpret_cast<typename C::Bars *>(reinterpret_cast<uint8_t *>(join) + C::JOIN);
   volatile int *abort = &bar->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(ring) & 1023u) {  // never: the declaration's alignment
+    if (tid == 0) report(a.err, PBS_ERR_DEVICE_ASSERT);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) mbar_init(&bar->full[i], 1), mbar_init(&bar->empty[i], 4);
     for (int i = 0; i < 2; ++i) {
@@ -89,6 +91,8 @@ __global__ void __launch_bounds__(MmaCfg<D, W>::THREADS, MmaCfg<D, W>::CTAS)
   allow_next();  // not before the wait: the next kernel looks at the lengths at once
   Place place;
   if (!find_place<ROWS, kKeys, C::THREADS>(a, bar->sum, &place)) return;
+  // r / G of a row r < 16 is r by_g >> 16
+  const unsigned by_g = 65536u / a.G + 1;
   // a tile in shared memory: [piece of a page][64-column half][row][128 bytes]
   const int box = min(a.page, kKeys);
 
@@ -117,10 +121,10 @@ __global__ void __launch_bounds__(MmaCfg<D, W>::THREADS, MmaCfg<D, W>::CTAS)
         mbar_arrive(&bar->q_full[slot]);
       }
       if (more) {
-        const int n = min(ROWS, g.count * a.G - g.rt * ROWS) * (D / 8);
+        const int n = g.count * a.G * (D / 8);
         for (int x = lane; x < n; x += 32) {  // rows behind: anything
           const int r = x / (D / 8), ch = x % (D / 8);
-          const int rr = g.rt * ROWS + r, i = rr / a.G, hd = g.h * a.G + rr - i * a.G;
+          const int i = r * by_g >> 16, hd = g.h * a.G + r - i * a.G;
           cp_async16(sQ + slot * ROWS * D + swz<D>(r, ch * 8),
                      (const T *)a.q.p + (int64_t)g.s * a.q.batch + hd * a.q.head + i * a.q.row +
                          ch * 8);
@@ -195,11 +199,11 @@ __global__ void __launch_bounds__(MmaCfg<D, W>::THREADS, MmaCfg<D, W>::CTAS)
     if (failed) return;
     const Segment g = bar->g[seg & 1];
     if (g.count == 0) return;
-    const int rows = min(ROWS, g.count * a.G - g.rt * ROWS);  // of this row tile
+    const int rows = g.count * a.G;  // one row tile an item
     const int len = g.start + g.count;
     int draft[2];  // of this thread's rows
 #pragma unroll
-    for (int x = 0; x < 2; ++x) draft[x] = min((g.rt * ROWS + gr + 8 * x) / a.G, g.count - 1);
+    for (int x = 0; x < 2; ++x) draft[x] = min((int)((gr + 8 * x) * by_g >> 16), g.count - 1);
     uint32_t q[D / 16][4];
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
@@ -362,15 +366,15 @@ __global__ void __launch_bounds__(MmaCfg<D, W>::THREADS, MmaCfg<D, W>::CTAS)
 #pragma unroll
           for (int e = 0; e < N; ++e) acc[e] += src[e] * f;
         }
-        const int rr = g.rt * ROWS + r;
         if (g.whole) {
+          const int i = r * by_g >> 16, hd = g.h * a.G + r - i * a.G;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
           for (int e = 0; e < N; ++e) acc[e] *= inv;
           if (any_bad())
-            add_wild<T, N>(a, g.s, g.h, Seq{g.start, g.count}, rr / a.G, D, col, acc);
-          write_row<T, N>(a, g.s, g.h, rr, D, col, acc);
-          if (col == 0) write_lse(a, g.s, g.h, rr, top, sum);
+            add_wild<T, N>(a, g.s, g.h, Seq{g.start, g.count}, i, D, col, acc);
+          write_row<T, N>(a, g.s, hd, i, D, col, acc);
+          if (col == 0) write_lse(a, g.s, hd, i, top, sum);
         } else {
           float *dst = reinterpret_cast<float *>(
               a.part_o + ((size_t)slot * (D / 4) + col / 4) * ROWS + r) + col % 4;
@@ -451,7 +455,7 @@ bool tree_supported(int hq, int tree, const pbs_cache &c) {
 //   4    8 x 16K                     91.9        89.4          -
 //   16   8 x 16K                     96.2        90.2          -
 //   4    64 x 1000                   54.4        75.4          -
-//   16   64 x 1000                   60.7        75.6          -
+//   16   64 x 1000                   58.6        75.6          -
 //   4    1 x 8K                      17.2        20.0          -
 //   32   8 x 16K                        -        94.1      107.5
 //   128  8 x 16K                        -       105.6      114.8
@@ -464,25 +468,27 @@ int row_tile(int hq, int tree, const pbs_cache &c) {
 }
 
 // Consumer warps of a CTA of the warp-MMA kernel: 8, or 4 in each of two CTAs an
-// SM. Two CTAs hide the 3 to 5 us that an item's beginning and end cost, and
+// SM. Two CTAs hide the 2 to 4 us that an item's beginning and end cost, and
 // have two warps to issue the copies, where 16-token pages of d = 64 keep one
 // busy; their twice as many runs leave more parts to join, and a long item reads
 // a little slower. Us a call (4 rows, 8 KV heads, captured):
-//   d, page   sequences x tokens    8 warps   2 x 4
-//   128, 64   2000 x 50               428.2   274.1
-//   128, 64   512 x 200               156.8   118.3
-//   128, 64   32 x 300                 21.9    18.3
-//   128, 64   64 x 1000                54.4    54.2
-//   128, 64   32 x 8000               171.3   171.8
-//   128, 64   64 x 4000               172.7   174.5
-//   128, 16   64 x 4000               167.8   172.5
-//   128, 64   1 x 32000                34.7    36.0
-//   64, 64    256 x 1000              118.4   100.4
-//   64, 64    32 x 8000                96.2    94.8
-//   64, 16    32 x 8000               142.3    89.5
-//   64, 16    1 x 32000                26.2    21.9
-//   64, 64    1 x 32000                22.3    22.5
-//   128, 64   1 x 131072, 1 KV head    32.5    46.0
+//   d, page   sequences x tokens       8 warps   2 x 4
+//   128, 64    2000 x 50                  395.8   227.3
+//   128, 64    512 x 200                  148.2   108.0
+//   128, 64    32 x 300                    20.6    17.7
+//   128, 64    32 x 500, 16 rows           31.2    25.9
+//   128, 64    64 x 1000                   53.7    54.8
+//   128, 64    64 x 1000, 16 rows          63.0    58.6
+//   128, 64    32 x 8000                  170.6   172.1
+//   128, 64    64 x 4000                  172.4   173.0
+//   128, 16    64 x 4000                  167.8   172.0
+//   128, 64    1 x 32000                   34.2    35.8
+//   128, 64    1 x 131072, 1 KV head       30.7    43.0
+//   64, 64     256 x 1000                 119.3   100.5
+//   64, 64     32 x 8000                   97.1    94.8
+//   64, 16     32 x 8000                  143.0    90.6
+//   64, 16     1 x 32000                   26.1    21.9
+//   64, 64     1 x 32000                   22.4    22.5
 // The lengths are on the device; the host knows the items (a KV head of a
 // sequence) and the most tokens that a table row can name.
 int mma_warps(const pbs_cache &c) {

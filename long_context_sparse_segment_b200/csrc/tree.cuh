@@ -329,12 +329,11 @@ __device__ __noinline__ void add_wild(const TreeArgs &a, int s, int h, const Seq
   }
 }
 
-// N output columns of row r of an item, from fp32.
+// N output columns of a query head's draft i, from fp32.
 template <typename T, int N>
-__device__ __forceinline__ void write_row(const TreeArgs &a, int s, int h, int r, int d, int col,
+__device__ __forceinline__ void write_row(const TreeArgs &a, int s, int head, int i, int d, int col,
                                           const float (&o)[N]) {
-  const int i = r / a.G, g = r % a.G;
-  T *dst = (T *)a.out + (((size_t)s * a.hq + h * a.G + g) * a.tree + i) * d + col;
+  T *dst = (T *)a.out + (((size_t)s * a.hq + head) * a.tree + i) * d + col;
   if constexpr (N == 1) {
     *reinterpret_cast<uint16_t *>(dst) = (uint16_t)Two<T>::pack(o[0], 0.f);
   } else {
@@ -350,9 +349,9 @@ __device__ __forceinline__ void write_row(const TreeArgs &a, int s, int h, int r
   }
 }
 
-__device__ __forceinline__ void write_lse(const TreeArgs &a, int s, int h, int r, float m, float l) {
+__device__ __forceinline__ void write_lse(const TreeArgs &a, int s, int head, int i, float m, float l) {
   if (a.lse)
-    a.lse[((size_t)s * a.hq + h * a.G + r % a.G) * a.tree + r / a.G] =
+    a.lse[((size_t)s * a.hq + head) * a.tree + i] =
         l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
@@ -401,9 +400,9 @@ __global__ void __launch_bounds__(kCombineThreads)
   for (int r0 = blockIdx.x * RB; r0 < all; r0 += gridDim.x * RB) {
     if (a.zero_rest && tid < E && r0 + er >= rows && r0 + er < all) {
       const float o[4] = {};
-      write_row<T, 4>(a, s, h, r0 + er, D, ec, o);
-      if (ec == 0 && a.lse)
-        a.lse[((size_t)s * a.hq + h * a.G + (r0 + er) % a.G) * a.tree + (r0 + er) / a.G] = 0.f;
+      const int i = (r0 + er) / a.G, head = h * a.G + (r0 + er) % a.G;
+      write_row<T, 4>(a, s, head, i, D, ec, o);
+      if (ec == 0 && a.lse) a.lse[((size_t)s * a.hq + head) * a.tree + i] = 0.f;
     }
     if (r0 >= rows) continue;
     const int2 item = a.items[((size_t)s * a.hkv + h) * a.tiles + r0 / ROWS];
@@ -448,9 +447,10 @@ __global__ void __launch_bounds__(kCombineThreads)
       const float4 v = so[tid];
       const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
       float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-      if (bad) add_wild<T, 4>(a, s, h, q, (r0 + er) / a.G, D, ec, o);
-      write_row<T, 4>(a, s, h, r0 + er, D, ec, o);
-      if (ec == 0) write_lse(a, s, h, r0 + er, ml.x, ml.y);
+      const int i = (r0 + er) / a.G, head = h * a.G + (r0 + er) % a.G;
+      if (bad) add_wild<T, 4>(a, s, h, q, i, D, ec, o);
+      write_row<T, 4>(a, s, head, i, D, ec, o);
+      if (ec == 0) write_lse(a, s, head, i, ml.x, ml.y);
     }
     __syncthreads();
   }

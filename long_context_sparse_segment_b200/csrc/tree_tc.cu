@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------- the item's end
     const int slot = 2 * blockIdx.x + (seg > 0);
     if (tid == 128) tell_item(a, g, sh->place.run, slot);
-    const int rr = g.rt * ROWS + row;
+    const int rr = g.rt * ROWS + row, i = rr / a.G, head = g.h * a.G + rr - i * a.G;
     float top = m_used, sum = l, f[2] = {1.f, 1.f};
     if (!PAIR) {
       // both streams' outputs, half of the columns by each group of warps;
@@ -568,8 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               float *w = o + e;
               float y[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
               if (bad)
-                add_wild<T, 8>(a, g.s, g.h, Seq{g.start, g.count}, rr / a.G, D, col + e, y);
-              write_row<T, 8>(a, g.s, g.h, rr, D, col + e, y);
+                add_wild<T, 8>(a, g.s, g.h, Seq{g.start, g.count}, i, D, col + e, y);
+              write_row<T, 8>(a, g.s, head, i, D, col + e, y);
             }
           } else {
             float4 *dst = a.part_o + ((size_t)slot * (D / 4) + col / 4) * ROWS + row;
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (row < rows && (PAIR || x == 0)) {
         if (g.whole)
-          write_lse(a, g.s, g.h, rr, top, sum);
+          write_lse(a, g.s, head, i, top, sum);
         else
           a.part_ml[(size_t)slot * ROWS + row] = make_float2(top, sum);
       }
