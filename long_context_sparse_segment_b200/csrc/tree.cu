@@ -471,7 +471,8 @@ int row_tile(int hq, int tree, const pbs_cache &c) {
 // SM. Two CTAs hide the 2 to 4 us that an item's beginning and end cost, and
 // have two warps to issue the copies, where 16-token pages of d = 64 keep one
 // busy; their twice as many runs leave more parts to join, and a long item reads
-// a little slower. Us a call (4 rows, 8 KV heads, captured):
+// a little slower. Us a call (4 rows, 8 KV heads, captured; one block a head
+// in the joining kernel, whose later form takes 37 off 2000 x 50, 8 off 512 x 200):
 //   d, page   sequences x tokens       8 warps   2 x 4
 //   128, 64    2000 x 50                  395.8   227.3
 //   128, 64    512 x 200                  148.2   108.0

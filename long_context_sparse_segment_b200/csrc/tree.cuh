@@ -361,12 +361,12 @@ __device__ __forceinline__ float part_scale(float m, float top) {
 }
 
 // -------------------------------------------------------------------- combine
-// Joins the parts of the rows that several CTAs worked on. A block takes every
-// gridDim.x-th group of RB rows of one (sequence, KV head): a thread holds 4
-// columns of a row and every PG-th part of it, in order; the PG partial results
-// are joined in shared memory. Bound by latency: a part is read once, a thread's
-// reads in flight together; most blocks find that nobody shared their items and
-// end.
+// Joins the parts of the rows that several CTAs worked on. A block takes groups
+// of RB rows of one (sequence, KV head), or with MANY of `heads` of them, one
+// after the other: a thread holds 4 columns of a row and every PG-th part of it,
+// in order; the PG partial results are joined in shared memory. Bound by latency:
+// a part is read once, a thread's reads in flight together; most blocks find that
+// nobody shared their items and end.
 constexpr int kCombineThreads = 512;
 
 struct Part {
@@ -381,78 +381,100 @@ __device__ __forceinline__ void join(Part &p, const Part &q) {
   p.o.z = p.o.z * f + q.o.z * g, p.o.w = p.o.w * f + q.o.w * g;
 }
 
-template <typename T, int D, int ROWS, int RB>
+template <typename T, int D, int ROWS, int RB, bool MANY>
 __global__ void __launch_bounds__(kCombineThreads)
-    tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
+    tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid, int heads) {
   constexpr int C4 = D / 4, E = RB * C4;  // results of a group, 4 columns each
   constexpr int PG = kCombineThreads / E;
   static_assert(PG * E == kCombineThreads && ROWS % RB == 0, "threads");
   __shared__ float4 so[kCombineThreads];
   __shared__ float2 sml[PG][RB];
-  const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
-  allow_next();
-  const Seq q = seq_of(a, s);  // the attention kernel has not changed it
-  const int rows = q.count * a.G, all = a.tree * a.G;  // of the (sequence, KV head)
+  const int tid = threadIdx.x, lane = tid & 31;
   const int r = tid % RB, c4 = tid / RB % C4, pg = tid / E;
   // results: neighbouring threads along a row
   const int er = tid / C4, ec = tid % C4 * 4;
+  allow_next();
+  // MANY: every warp finds those of the block's heads that have something to do
+  const int first = blockIdx.x * heads;
+  const int pair = MANY ? min(first + lane, a.seqs * a.hkv - 1) : 0;
+  // the attention kernel has not changed the lengths
+  const Seq own = seq_of(a, MANY ? pair / a.hkv : blockIdx.z);
   wait_previous();
-  for (int r0 = blockIdx.x * RB; r0 < all; r0 += gridDim.x * RB) {
-    if (a.zero_rest && tid < E && r0 + er >= rows && r0 + er < all) {
-      const float o[4] = {};
-      const int i = (r0 + er) / a.G, head = h * a.G + (r0 + er) % a.G;
-      write_row<T, 4>(a, s, head, i, D, ec, o);
-      if (ec == 0 && a.lse) a.lse[((size_t)s * a.hq + head) * a.tree + i] = 0.f;
+  unsigned todo = 1;
+  if constexpr (MANY) {
+    bool need = a.zero_rest && own.count < a.tree;
+    for (int t = 0; t < cdiv(own.count * a.G, ROWS) && !need; ++t) {
+      const int2 item = a.items[(size_t)pair * a.tiles + t];
+      need = item.x >> 1 != item.y;
     }
-    if (r0 >= rows) continue;
-    const int2 item = a.items[((size_t)s * a.hkv + h) * a.tiles + r0 / ROWS];
-    const int slot0 = item.x, c0 = slot0 >> 1, c1 = item.y;
-    if (c0 == c1) continue;
-    if (c0 < 0 || c1 < c0 || c1 >= grid) {  // the attention kernel gave up before
-      if (tid == 0) report(a.err, PBS_ERR_DEVICE_ASSERT);
-      continue;
-    }
-    Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    int bad = 0;
-    if (r0 + r < rows) {
-      const int rr = r0 % ROWS + r;
-#pragma unroll 4
-      for (int c = c0 + pg; c <= c1; c += PG) {
-        const size_t slot = c == c0 ? slot0 : 2 * c;
-        const float2 ml = a.part_ml[slot * ROWS + rr];
-        join(p, Part{ml.x, ml.y, a.part_o[(slot * C4 + c4) * ROWS + rr]});
-        bad |= a.part_bad[slot];
+    todo = __ballot_sync(0xffffffffu, need && lane < heads && pair == first + lane);
+  }
+  for (; todo; todo &= todo - 1) {
+    const int at = MANY ? __ffs(todo) - 1 : 0;
+    const int s = MANY ? (first + at) / a.hkv : blockIdx.z;
+    const int h = MANY ? (first + at) % a.hkv : blockIdx.y;
+    const Seq q = MANY ? Seq{__shfl_sync(0xffffffffu, own.start, at),
+                             __shfl_sync(0xffffffffu, own.count, at)}
+                       : own;
+    const int rows = q.count * a.G, all = a.tree * a.G;  // of the (sequence, KV head)
+    const int group = MANY ? blockIdx.y : blockIdx.x, groups = MANY ? gridDim.y : gridDim.x;
+    for (int r0 = group * RB; r0 < all; r0 += groups * RB) {
+      if (a.zero_rest && tid < E && r0 + er >= rows && r0 + er < all) {
+        const float o[4] = {};
+        const int i = (r0 + er) / a.G, head = h * a.G + (r0 + er) % a.G;
+        write_row<T, 4>(a, s, head, i, D, ec, o);
+        if (ec == 0 && a.lse) a.lse[((size_t)s * a.hq + head) * a.tree + i] = 0.f;
       }
-    }
-    if (PG > 1) {
-      so[tid] = p.o;
-      if (c4 == 0) sml[pg][r] = make_float2(p.m, p.l);
-    }
-    bad = __syncthreads_or(bad);
-    if (PG > 1) {
-      if (pg == 0) {
+      if (r0 >= rows) continue;
+      const int2 item = a.items[((size_t)s * a.hkv + h) * a.tiles + r0 / ROWS];
+      const int slot0 = item.x, c0 = slot0 >> 1, c1 = item.y;
+      if (c0 == c1) continue;
+      if (c0 < 0 || c1 < c0 || c1 >= grid) {  // the attention kernel gave up before
+        if (tid == 0) report(a.err, PBS_ERR_DEVICE_ASSERT);
+        continue;
+      }
+      Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      int bad = 0;
+      if (r0 + r < rows) {
+        const int rr = r0 % ROWS + r;
+#pragma unroll 4
+        for (int c = c0 + pg; c <= c1; c += PG) {
+          const size_t slot = c == c0 ? slot0 : 2 * c;
+          const float2 ml = a.part_ml[slot * ROWS + rr];
+          join(p, Part{ml.x, ml.y, a.part_o[(slot * C4 + c4) * ROWS + rr]});
+          bad |= a.part_bad[slot];
+        }
+      }
+      if (PG > 1) {
+        so[tid] = p.o;
+        if (c4 == 0) sml[pg][r] = make_float2(p.m, p.l);
+      }
+      bad = __syncthreads_or(bad);
+      if (PG > 1) {
+        if (pg == 0) {
 #pragma unroll
-        for (int g = 1; g < PG; ++g)
-          join(p, Part{sml[g][r].x, sml[g][r].y, so[tid + g * E]});
+          for (int g = 1; g < PG; ++g)
+            join(p, Part{sml[g][r].x, sml[g][r].y, so[tid + g * E]});
+        }
+        __syncthreads();
+      }
+      if (pg == 0) {
+        so[r * C4 + c4] = p.o;
+        if (c4 == 0) sml[0][r] = make_float2(p.m, p.l);
+      }
+      __syncthreads();
+      if (tid < E && r0 + er < rows) {
+        const float2 ml = sml[0][er];
+        const float4 v = so[tid];
+        const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+        float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+        const int i = (r0 + er) / a.G, head = h * a.G + (r0 + er) % a.G;
+        if (bad) add_wild<T, 4>(a, s, h, q, i, D, ec, o);
+        write_row<T, 4>(a, s, head, i, D, ec, o);
+        if (ec == 0) write_lse(a, s, head, i, ml.x, ml.y);
       }
       __syncthreads();
     }
-    if (pg == 0) {
-      so[r * C4 + c4] = p.o;
-      if (c4 == 0) sml[0][r] = make_float2(p.m, p.l);
-    }
-    __syncthreads();
-    if (tid < E && r0 + er < rows) {
-      const float2 ml = sml[0][er];
-      const float4 v = so[tid];
-      const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
-      float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-      const int i = (r0 + er) / a.G, head = h * a.G + (r0 + er) % a.G;
-      if (bad) add_wild<T, 4>(a, s, h, q, i, D, ec, o);
-      write_row<T, 4>(a, s, head, i, D, ec, o);
-      if (ec == 0) write_lse(a, s, head, i, ml.x, ml.y);
-    }
-    __syncthreads();
   }
 }
 
@@ -464,13 +486,24 @@ cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
   // for four such rounds, then they walk the groups.
   const int64_t rows = (int64_t)a.G * a.tree, heads = (int64_t)a.hkv * a.seqs, fit = 4 * 148;
   const int rb = ceil_div(rows, 4) * heads <= fit ? 4 : 16;
-  int64_t gx = ceil_div(rows, rb);
-  if (gx * heads > 4 * fit) gx = ceil_div(4 * fit, heads);
-  const dim3 blocks((unsigned)gx, a.hkv, a.seqs);
-  return rb == 4 ? launch_behind(tree_combine_kernel<T, D, ROWS, 4>, blocks, kCombineThreads, 0,
-                                 st, a, grid)
-                 : launch_behind(tree_combine_kernel<T, D, ROWS, 16>, blocks, kCombineThreads, 0,
-                                 st, a, grid);
+  int64_t groups = ceil_div(rows, rb);
+  // Where that is more than one round and the heads are twice the CTAs, a block
+  // looks after several heads, of which no more than one is cut on average (a
+  // block a head is 37 us slower behind 16000 heads, 65 behind 4096 of 256 rows;
+  // the same code for one head costs 16 registers, a block an SM).
+  if (groups * heads > fit && heads >= 2 * grid) {
+    const int64_t per = heads / grid > 32 ? 32 : heads / grid, gx = ceil_div(heads, per);
+    if (groups * gx > 4 * fit) groups = ceil_div(4 * fit, gx);
+    return launch_behind(tree_combine_kernel<T, D, ROWS, 16, true>,
+                         dim3((unsigned)gx, (unsigned)groups), kCombineThreads, 0, st, a, grid,
+                         (int)per);
+  }
+  if (groups * heads > 4 * fit) groups = ceil_div(4 * fit, heads);
+  const dim3 blocks((unsigned)groups, a.hkv, a.seqs);
+  return rb == 4 ? launch_behind(tree_combine_kernel<T, D, ROWS, 4, false>, blocks,
+                                 kCombineThreads, 0, st, a, grid, 1)
+                 : launch_behind(tree_combine_kernel<T, D, ROWS, 16, false>, blocks,
+                                 kCombineThreads, 0, st, a, grid, 1);
 }
 
 }  // namespace tree

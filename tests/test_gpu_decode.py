@@ -705,6 +705,27 @@ def test_many_short_sequences(d, seqs, hkv, g, tree, most, page, dtype, dev):
     assert torch.equal(bits(o), bits(again[0])) and torch.equal(bits(lse), bits(again[1]))
 
 
+@pytest.mark.parametrize("tree,g,most", [(12, 3, 300), (90, 3, 200), (64, 2, 150), (3, 2, 400)])
+def test_drafts_of_many_sequences(tree, g, most, dev):
+    """Far more items than CTAs, some of them cut, rows behind the counts zeroed
+    or left as they were."""
+    r, seqs, hkv, d = random.Random(tree), 221, 3, 64
+    start = [r.randint(0, most) for _ in range(seqs)]
+    count = [r.choice([0, 1, tree, r.randint(0, tree)]) for _ in range(seqs)]
+    t = Tree(dev, BF16, d, 32, hkv, start, count, tree, tree)
+    q = (2 * torch.randn(seqs, hkv * g, tree, d, generator=torch.Generator().manual_seed(4)))
+    q = q.to(BF16).to(dev)
+    o, lse = pbs.tree_attn(q, t.k, t.v, t.table, i32(start, dev), None, i32(count, dev), lse=True)
+    assert pbs.device_status() == 0
+    t.check(q, o, lse, chains(tree, count), 1 / math.sqrt(d), BF16)
+    kept = torch.full_like(o, 7.0)
+    pbs.tree_attn(q, t.k, t.v, t.table, i32(start, dev), None, i32(count, dev), out=kept)
+    for s in range(seqs):
+        assert not o[s, :, count[s]:].any() and not lse[s, :, count[s]:].any()
+        assert torch.equal(bits(kept[s, :, :count[s]]), bits(o[s, :, :count[s]]))
+        assert (kept[s, :, count[s]:] == 7).all()
+
+
 @pytest.mark.parametrize("d,seqs,hkv,tokens", [(64, 1, 8, 130), (128, 64, 8, 130), (128, 2, 8, 9000),
                                                (64, 2, 8, 9000)])
 @pytest.mark.parametrize("tree", [1, 9, 64])
