@@ -565,7 +565,9 @@ pbs_status pbs_cache_compact(void *k_pages, void *v_pages, int32_t *table, int32
  * sequence whose path does not, or names a token that no page holds, is
  * reported and left alone.
  * The pages from token start[s] on must be the sequence's own (reserved).
- * lens (may be NULL): lens[s] = start[s] + count[s] where the path is good.
+ * lens (may be NULL): lens[s] = start[s] + count[s] where the path is good. It
+ * may be start itself, or count (the lengths are then written by a second
+ * kernel), and reaches into no other input.
  */
 pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,
                             const int32_t *start, const int32_t *path, const int32_t *count,

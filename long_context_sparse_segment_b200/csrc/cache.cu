@@ -411,6 +411,20 @@ __global__ void __launch_bounds__(256)
 constexpr int kRows = 8;
 constexpr int kAcceptThreads = 128;  // rows whose places are held at a time, too
 
+// Row i of an accepted path `p`, which moves from token st + p[i] to st + i: the
+// words of both. False for a row that may not move.
+__device__ __forceinline__ bool accept_row(const int32_t *row, const int32_t *__restrict__ p, int i,
+                                           int st, const pbs_cache &c, int words, int64_t *from,
+                                           int64_t *to) {
+  const int x = __ldg(p + i), before = i > 0 ? __ldg(p + i - 1) : -1;
+  if (x < 0 || before >= x) return false;
+  *from = token_word(row, (int64_t)st + x, c, words);
+  *to = token_word(row, (int64_t)st + i, c, words);
+  const bool good = *from >= 0 && *to >= 0;
+  if (x == i) *to = -1;  // stays
+  return good;
+}
+
 __global__ void __launch_bounds__(kAcceptThreads)
     accept_kernel(uint4 *k, uint4 *v, const int32_t *__restrict__ table,
                   const int32_t *__restrict__ start, const int32_t *__restrict__ path,
@@ -424,15 +438,7 @@ __global__ void __launch_bounds__(kAcceptThreads)
   const int words = c.d / 8;
   // the places of rows i0 .. i0 + 127; false for a row that may not move
   auto look_up = [&](int i0) {
-    const int i = i0 + tid;
-    if (i >= n) return true;
-    const int x = __ldg(p + i), before = i > 0 ? __ldg(p + i - 1) : -1;
-    if (x < 0 || before >= x) return false;
-    const int64_t a = token_word(row, (int64_t)st + x, c, words);
-    const int64_t b = token_word(row, (int64_t)st + i, c, words);
-    from[tid] = a;
-    to[tid] = x == i ? -1 : b;
-    return a >= 0 && b >= 0;
+    return i0 + tid >= n || accept_row(row, p, i0 + tid, st, c, words, &from[tid], &to[tid]);
   };
   bool bad = st < 0;
   for (int i0 = (n - 1) / kAcceptThreads * kAcceptThreads; i0 >= 0; i0 -= kAcceptThreads)
@@ -463,6 +469,29 @@ __global__ void __launch_bounds__(kAcceptThreads)
         if (i0 + j0 + x < n && to[j0 + x] >= 0) pool[to[j0 + x]] = r[x];
     }
   }
+}
+
+// The lengths behind an acceptance whose `start` or `count` is `lens` itself: the
+// rows' kernel reads those in every block of a sequence until its end, so the
+// lengths are written behind it, where the path is good (one block a sequence, 2 us).
+__global__ void __launch_bounds__(kAcceptThreads)
+    accept_lens_kernel(const int32_t *__restrict__ table, const int32_t *start,
+                       const int32_t *__restrict__ path, const int32_t *count, int32_t *lens,
+                       int tree, pbs_cache c) {
+  const int s = blockIdx.x;
+  const int n = count ? min(count[s], tree) : tree, st = start[s];
+  bool bad = st < 0;
+  for (int i = threadIdx.x; i < n; i += kAcceptThreads) {
+    int64_t from, to;
+    bad |= !accept_row(table + (size_t)s * c.width, path + (size_t)s * tree, i, st, c, c.d / 8,
+                       &from, &to);
+  }
+  if (!__syncthreads_or(bad) && threadIdx.x == 0) lens[s] = st + max(n, 0);
+}
+
+// Whether [a, a + an) and [b, b + bn) meet; a null one meets nothing.
+bool meet(const void *a, size_t an, const void *b, size_t bn) {
+  return a && b && (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
 }
 
 bool cache_ok(const pbs_cache &c) {
@@ -616,12 +645,22 @@ pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,
   if (!pool_ok(k_pages) || !pool_ok(v_pages) || k_pages == v_pages || !ints_ok(table) ||
       !ints_ok(start) || !ints_ok(path) || (count && !ints_ok(count)) || (lens && !ints_ok(lens)))
     return PBS_ERR_INVALID_ARG;
+  // lens may be start or count, but otherwise nothing that other sequences read
+  const size_t each = 4 * (size_t)c.seqs;
+  if ((lens != start && meet(lens, each, start, each)) ||
+      (lens != count && meet(lens, each, count, each)) || meet(lens, each, path, each * tree) ||
+      meet(lens, each, table, each * c.width))
+    return PBS_ERR_INVALID_ARG;
   const int col_blocks = (int)ceil_div((int64_t)c.hkv * (c.d / 8), kAcceptThreads);
   const int64_t gx = 2LL * c.layers * col_blocks;
   if (gx > 0x7fffffff) return PBS_ERR_UNSUPPORTED;
+  const bool behind = lens && (lens == start || lens == count);
   accept_kernel<<<dim3((unsigned)gx, c.seqs), kAcceptThreads, 0, (cudaStream_t)st>>>(
-      (uint4 *)k_pages, (uint4 *)v_pages, table, start, path, count, lens, tree, c, col_blocks,
-      error_word());
+      (uint4 *)k_pages, (uint4 *)v_pages, table, start, path, count, behind ? nullptr : lens, tree,
+      c, col_blocks, error_word());
+  if (behind)
+    accept_lens_kernel<<<c.seqs, kAcceptThreads, 0, (cudaStream_t)st>>>(table, start, path, count,
+                                                                       lens, tree, c);
   return done();
 }
 

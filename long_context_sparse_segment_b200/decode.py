@@ -383,7 +383,8 @@ def cache_accept(k_pages, v_pages, table, start, path, count=None, lens=None):
     """The accepted drafts moved behind their prefix: token start[s] +
     path[s][i] becomes token start[s] + i, i < count[s], in every layer
     (pbs_cache_accept). path [seqs, n] ascends strictly (n may be less than the
-    drafts). With ``lens``, lens[s] becomes start[s] + count[s]."""
+    drafts). With ``lens``, lens[s] becomes start[s] + count[s]; it may be
+    ``start`` itself (the drafts' start is the length), or ``count``."""
     c = _pools(k_pages, v_pages, table)
     dev = k_pages.device
     _ints(start, "start", (c.seqs,), dev)
@@ -508,8 +509,7 @@ class PagedCache:
 
     def accept(self, path, count=None):
         """The accepted drafts behind the lengths, which grow by their number."""
-        start = self.lens.clone()
-        cache_accept(self.k, self.v, self.table, start, path, count, self.lens)
+        cache_accept(self.k, self.v, self.table, self.lens, path, count, self.lens)
 
     def fork(self, src, dst):
         cache_fork(self.table, self.refs, self.lens, src, dst, self.page)
