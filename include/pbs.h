@@ -481,6 +481,12 @@ typedef struct {
   int page; /* tokens per page */
   int d;    /* a multiple of 8; 64 or 128 for pbs_tree_attn */
   int seqs, width;
+  /* NULL, or the reference counts for pbs_cache_append and pbs_cache_accept
+   * (the calls that take refs of their own do not read it): they then write
+   * only into pages that one sequence holds alone, refs == 1, and report and
+   * leave the others. So a pbs_cache_reserve that found too few free pages
+   * cannot end in writes to another sequence's tokens. */
+  const int32_t *refs;
 } pbs_cache;
 
 typedef enum {
@@ -514,7 +520,8 @@ pbs_status pbs_cache_reserve(int32_t *table, int32_t *refs, const int32_t *lens,
  * pbs_cache_append - rows i < count[s] (all n when count is NULL) of k, v
  * [layers, seqs, hkv, n, d] written at tokens start[s] + i. The pages must
  * be reserved, k and v lie outside the pools, the pools apart. No other row of
- * the pools is touched.
+ * the pools is touched. Rows without a page, or with c.refs on a page that
+ * several sequences hold, are reported and skipped.
  */
 pbs_status pbs_cache_append(pbs_rows k, pbs_rows v, int n, void *k_pages, void *v_pages,
                             const int32_t *table, const int32_t *start, const int32_t *count,
@@ -564,7 +571,9 @@ pbs_status pbs_cache_compact(void *k_pages, void *v_pages, int32_t *table, int32
  * [seqs, n] ascends strictly from 0 on, so a draft only moves down; a
  * sequence whose path does not, or names a token that no page holds, is
  * reported and left alone.
- * The pages from token start[s] on must be the sequence's own (reserved).
+ * The pages from token start[s] on must be the sequence's own (reserved); with
+ * c.refs a sequence whose accepted tokens come to lie in a page that several
+ * hold is reported and left alone too.
  * lens (may be NULL): lens[s] = start[s] + count[s] where the path is good. It
  * may be start itself, or count (the lengths are then written by a second
  * kernel), and reaches into no other input.

@@ -44,7 +44,7 @@ class Rows(ctypes.Structure):
 class Cache(ctypes.Structure):
     _fields_ = [("layers", ctypes.c_int), ("pages", ctypes.c_int), ("hkv", ctypes.c_int),
                 ("page", ctypes.c_int), ("d", ctypes.c_int), ("seqs", ctypes.c_int),
-                ("width", ctypes.c_int)]
+                ("width", ctypes.c_int), ("refs", ctypes.c_void_p)]
 
 
 class PbsError(RuntimeError):

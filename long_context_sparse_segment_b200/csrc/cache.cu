@@ -359,14 +359,16 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 // ------------------------------------------------------------ append, accept
 // The word offset of token t of sequence s in one layer's pool (head 0, first
-// word), or -1 for a token that no page holds.
+// word), or -1 for a token that no page holds; `write`: or, with c.refs, one
+// whose page is not the sequence's alone.
 __device__ __forceinline__ int64_t token_word(const int32_t *row, int64_t t, const pbs_cache &c,
-                                              int words) {
+                                              int words, bool write) {
   if (t < 0 || t > 0x7fffffff) return -1;
   const unsigned j = (unsigned)t / (unsigned)c.page;
   if (j >= (unsigned)c.width) return -1;
   const int page = row[j];
   if (page < 0 || page >= c.pages) return -1;
+  if (write && c.refs && c.refs[page] != 1) return -1;
   return ((int64_t)page * c.hkv * c.page + ((unsigned)t - j * c.page)) * words;
 }
 
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(256)
     x /= c.hkv;
     const int s = (int)(x % c.seqs), l = (int)(x / c.seqs);
     if (count && i >= count[s]) continue;
-    const int64_t o = token_word(table + (size_t)s * c.width, (int64_t)start[s] + i, c, words);
+    const int64_t o = token_word(table + (size_t)s * c.width, (int64_t)start[s] + i, c, words, true);
     if (o < 0) {
       report(err, PBS_ERR_DEVICE_ASSERT);
       continue;
@@ -418,8 +420,8 @@ __device__ __forceinline__ bool accept_row(const int32_t *row, const int32_t *__
                                            int64_t *to) {
   const int x = __ldg(p + i), before = i > 0 ? __ldg(p + i - 1) : -1;
   if (x < 0 || before >= x) return false;
-  *from = token_word(row, (int64_t)st + x, c, words);
-  *to = token_word(row, (int64_t)st + i, c, words);
+  *from = token_word(row, (int64_t)st + x, c, words, false);
+  *to = token_word(row, (int64_t)st + i, c, words, true);
   const bool good = *from >= 0 && *to >= 0;
   if (x == i) *to = -1;  // stays
   return good;
@@ -556,7 +558,8 @@ pbs_status pbs_cache_append(pbs_rows k, pbs_rows v, int n, void *k_pages, void *
   if (!cache_ok(c) || n < 0) return PBS_ERR_INVALID_ARG;
   if (c.seqs == 0 || n == 0) return PBS_OK;
   if (!rows_ok(k, 2) || !rows_ok(v, 2) || !pool_ok(k_pages) || !pool_ok(v_pages) ||
-      k_pages == v_pages || !ints_ok(table) || !ints_ok(start) || (count && !ints_ok(count)))
+      k_pages == v_pages || !ints_ok(table) || !ints_ok(start) || (count && !ints_ok(count)) ||
+      (c.refs && !ints_ok(c.refs)))
     return PBS_ERR_INVALID_ARG;
   const int64_t total = (int64_t)c.layers * c.seqs * c.hkv * n * (c.d / 8);
   const int64_t blocks = ceil_div(total, 256), most = 148 * 32;
@@ -643,13 +646,14 @@ pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,
   if (c.seqs == 0 || tree == 0) return PBS_OK;
   // one pool for both would be moved twice at once
   if (!pool_ok(k_pages) || !pool_ok(v_pages) || k_pages == v_pages || !ints_ok(table) ||
-      !ints_ok(start) || !ints_ok(path) || (count && !ints_ok(count)) || (lens && !ints_ok(lens)))
+      !ints_ok(start) || !ints_ok(path) || (count && !ints_ok(count)) || (lens && !ints_ok(lens)) ||
+      (c.refs && !ints_ok(c.refs)))
     return PBS_ERR_INVALID_ARG;
   // lens may be start or count, but otherwise nothing that other sequences read
   const size_t each = 4 * (size_t)c.seqs;
   if ((lens != start && meet(lens, each, start, each)) ||
       (lens != count && meet(lens, each, count, each)) || meet(lens, each, path, each * tree) ||
-      meet(lens, each, table, each * c.width))
+      meet(lens, each, table, each * c.width) || meet(lens, each, c.refs, 4 * (size_t)c.pages))
     return PBS_ERR_INVALID_ARG;
   const int col_blocks = (int)ceil_div((int64_t)c.hkv * (c.d / 8), kAcceptThreads);
   const int64_t gx = 2LL * c.layers * col_blocks;

@@ -312,10 +312,19 @@ def cache_reserve(table, refs, lens, want, page):
     return src, dst
 
 
-def cache_append(k, v, k_pages, v_pages, table, start, count=None):
+def _owned(c, refs, device):
+    """``refs`` put into c: writes only into pages that one sequence holds alone."""
+    if refs is not None:
+        _ints(refs, "refs", (c.pages,), device)
+        c.refs = refs.data_ptr()
+
+
+def cache_append(k, v, k_pages, v_pages, table, start, count=None, refs=None):
     """Rows i < count[s] (all without count) of k, v [seqs, hkv, n, d] written
     at tokens start[s] + i of one layer's pools, or [layers, seqs, hkv, n, d]
-    of all layers (pbs_cache_append). The pages must be reserved."""
+    of all layers (pbs_cache_append). The pages must be reserved; with ``refs``
+    rows whose page another sequence holds too, as behind a reserve that found
+    too few free pages, are reported and skipped."""
     c = _pools(k_pages, v_pages, table)
     dev = k_pages.device
     for t, nm in ((k, "k"), (v, "v")):
@@ -328,6 +337,7 @@ def cache_append(k, v, k_pages, v_pages, table, start, count=None):
     _ints(start, "start", (c.seqs,), dev)
     if count is not None:
         _ints(count, "count", (c.seqs,), dev)
+    _owned(c, refs, dev)
     if k.numel() == 0:
         return
     _call("pbs_cache_append", dev, _rows(k, "k"), _rows(v, "v"), k.shape[-2], _ptr(k_pages),
@@ -379,12 +389,14 @@ def cache_compact(k_pages, v_pages, table, refs):
     return src, dst
 
 
-def cache_accept(k_pages, v_pages, table, start, path, count=None, lens=None):
+def cache_accept(k_pages, v_pages, table, start, path, count=None, lens=None, refs=None):
     """The accepted drafts moved behind their prefix: token start[s] +
     path[s][i] becomes token start[s] + i, i < count[s], in every layer
     (pbs_cache_accept). path [seqs, n] ascends strictly (n may be less than the
     drafts). With ``lens``, lens[s] becomes start[s] + count[s]; it may be
-    ``start`` itself (the drafts' start is the length), or ``count``."""
+    ``start`` itself (the drafts' start is the length), or ``count``. With
+    ``refs`` a sequence whose accepted tokens come to lie in a page that another
+    one holds too is reported and left alone."""
     c = _pools(k_pages, v_pages, table)
     dev = k_pages.device
     _ints(start, "start", (c.seqs,), dev)
@@ -394,6 +406,7 @@ def cache_accept(k_pages, v_pages, table, start, path, count=None, lens=None):
     for t, nm in ((count, "count"), (lens, "lens")):
         if t is not None:
             _ints(t, nm, (c.seqs,), dev)
+    _owned(c, refs, dev)
     _call("pbs_cache_accept", dev, _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(start),
           _ptr(path), _ptr(count), _ptr(lens), path.shape[1], c)
 
@@ -492,7 +505,8 @@ class PagedCache:
 
     def reserve(self, want):
         """Room for want[s] tokens in every sequence, shared pages that will
-        be written copied."""
+        be written copied. Too few free pages: nothing changes, and what append
+        and accept would then write into a shared page is reported and left out."""
         src, dst = cache_reserve(self.table, self.refs, self.lens, want, self.page)
         cache_copy(self.k, self.v, src, dst)
 
@@ -500,7 +514,7 @@ class PagedCache:
         """k, v [seqs, hkv, n, d] at tokens start[s].. (the length) of a layer.
         The length is not changed: every layer appends at the same tokens."""
         cache_append(k, v, self.k[layer], self.v[layer], self.table,
-                     self.lens if start is None else start, count)
+                     self.lens if start is None else start, count, self.refs)
 
     def attend(self, layer, q, mask=None, start=None, **kw):
         """tree_attn of a layer; ``start`` is the lengths when not given."""
@@ -509,7 +523,8 @@ class PagedCache:
 
     def accept(self, path, count=None):
         """The accepted drafts behind the lengths, which grow by their number."""
-        cache_accept(self.k, self.v, self.table, self.lens, path, count, self.lens)
+        cache_accept(self.k, self.v, self.table, self.lens, path, count, self.lens,
+                     self.refs)
 
     def fork(self, src, dst):
         cache_fork(self.table, self.refs, self.lens, src, dst, self.page)

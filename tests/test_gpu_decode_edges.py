@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import long_context_sparse_segment_b200 as pbs
+from long_context_sparse_segment_b200 import _lib
 from test_gpu_decode import bits, i32, ids
 
 pytestmark = pytest.mark.gpu
@@ -72,3 +73,52 @@ def test_accept_refuses_lengths_inside_other_inputs(dev):
                dict(start=x[:2], lens=table.view(-1)[2:])):
         with pytest.raises(pbs.PbsError):
             pbs.cache_accept(k, v, table, **dict(dict(path=path), **kw))
+
+
+@pytest.mark.parametrize("whole", [False, True])
+def test_nothing_is_written_into_shared_pages_behind_a_failed_reserve(whole, dev):
+    """A fork cut back to the middle of a shared page, a full pool, and the calls
+    enqueued behind the reserve that fails: the other holder's rows stay, rows
+    of pages that one sequence holds alone are written. By PagedCache and by the
+    functions on every layer at once."""
+    page, hkv, d, layers = 16, 2, 64, 3
+    c = pbs.PagedCache(3, 112, 8, hkv, d, page, layers, BF16, dev)
+    c.reserve(i32([100, 0, 12], dev))  # all 8 pages
+    c.k.copy_(ids(c.k.shape, dev, seed=1)), c.v.copy_(ids(c.v.shape, dev, seed=2))
+    c.lens.copy_(i32([100, 0, 10], dev))
+    c.fork(i32([0], dev), i32([1], dev))
+    c.trim(i32([-1, 50, -1], dev))
+    assert pbs.device_status() == 0
+    want = [bits(x).clone() for x in (c.k, c.v)]
+    new = ids((layers, 3, hkv, 10, d), dev, seed=3)
+    at = int(c.table[2, 0])
+    for w in want:
+        w[:, at, :, 10:12] = bits(new)[:, 2, :, :2]
+    books = [x.clone() for x in (c.table, c.refs)]
+    count = i32([0, 10, 2], dev)
+    c.reserve(c.lens + count)
+    if whole:
+        pbs.cache_append(new, new, c.k, c.v, c.table, c.lens, count, refs=c.refs)
+        for w in want:  # draft 1 behind token 9 + 1
+            w[:, at, :, 10] = w[:, at, :, 11]
+        pbs.cache_accept(c.k, c.v, c.table, c.lens, i32([[0, 2, 5], [0, 2, 5], [1, 0, 0]], dev),
+                         i32([0, 3, 1], dev), c.lens, refs=c.refs)
+        lens = [100, 50, 11]
+    else:
+        for l in range(layers):
+            c.append(l, new[l], new[l], count=count)
+        # a path that moves nothing makes no length of tokens that were not written
+        c.accept(i32([[0, 1, 2]] * 3, dev), i32([0, 3, 2], dev))
+        lens = [100, 50, 12]
+    assert pbs.device_status() == _lib.ERR_PAGES
+    assert all(torch.equal(a, b) for a, b in zip((c.table, c.refs), books))
+    assert torch.equal(bits(c.k), want[0]) and torch.equal(bits(c.v), want[1])
+    assert c.lens.tolist() == lens
+    # with a page free the same calls go through
+    c.trim(i32([-1, -1, 0], dev))
+    c.reserve(i32([0, 60, 0], dev))
+    c.append(0, new[0], new[0], count=i32([0, 10, 0], dev))
+    assert pbs.device_status() == 0
+    mine, theirs = int(c.table[1, 3]), int(c.table[0, 3])
+    assert mine == at and torch.equal(bits(c.k)[:, theirs], want[0][:, theirs])
+    assert torch.equal(bits(c.k)[0, mine, :, 2:12], bits(new)[0, 1])
