@@ -437,8 +437,9 @@ def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.
     start[s] + j, j < count[s], whose bit is set in mask row i (see
     ``tree_mask``; without mask j <= i). With tree = 1 this is a decoding
     step. Returns o [seqs, hq, tree, d], and lse [seqs, hq, tree] fp32 when
-    asked; rows i >= count[s] are left as they were in ``out`` and are zero
-    in what this call allocates (their lse too)."""
+    asked; rows i >= count[s], and a sequence that is refused on the device
+    (a negative length, tokens beyond the table), are left as they were in
+    ``out`` and are zero in what this call allocates (their lse too)."""
     c = _pools(k_pages, v_pages, table)
     dev, t, size = k_pages.device, k_pages.dtype, getattr(q, "shape", None)
     _on(q, "q", dev)
@@ -457,8 +458,8 @@ def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.
         _ints(count, "count", (seqs,), dev)
     if mask is not None:
         _ints(mask, "mask", (seqs, tree, (tree + 31) // 32), dev)
-    zero = count is not None and out is None
-    if out is None:
+    zero = out is None  # sequences that the kernel refuses have rows behind their count too
+    if zero:
         out = _fresh(q)
     else:
         _on(out, "out", dev)
@@ -467,9 +468,8 @@ def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.
         _apart(out, "out", q, k_pages, v_pages)
     l = None
     if lse:
-        l = out.new_empty((seqs, hq, tree), dtype=torch.float32)
-        if count is not None and not zero:
-            l.zero_()
+        make = out.new_empty if zero else out.new_zeros
+        l = make((seqs, hq, tree), dtype=torch.float32)
     if not (seqs and tree):
         return (out, l) if lse else out
     need = lib().pbs_tree_workspace_bytes(hq, tree, c)

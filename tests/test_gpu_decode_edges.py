@@ -8,7 +8,7 @@ import torch
 
 import long_context_sparse_segment_b200 as pbs
 from long_context_sparse_segment_b200 import _lib
-from test_gpu_decode import bits, i32, ids
+from test_gpu_decode import Tree, bits, i32, ids
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,30 @@ def test_nothing_is_written_into_shared_pages_behind_a_failed_reserve(whole, dev
     mine, theirs = int(c.table[1, 3]), int(c.table[0, 3])
     assert mine == at and torch.equal(bits(c.k)[:, theirs], want[0][:, theirs])
     assert torch.equal(bits(c.k)[0, mine, :, 2:12], bits(new)[0, 1])
+
+
+# ------------------------------------------------------------------- attention
+@pytest.mark.parametrize("tree", [1, 9, 70])
+def test_refused_sequences_are_zero_in_what_is_allocated(tree, dev):
+    """A sequence beyond its table and one of negative length, without a count:
+    0 in allocated outputs, untouched in a given one, whose lse is 0."""
+    t = Tree(dev, BF16, 64, 16, 1, [20, 5, 9], [tree] * 3, tree, junk=False)
+    q = torch.randn(3, 2, tree, 64, device=dev).to(BF16)
+    start = i32([16 * t.table.shape[1], 5, -1], dev)
+    good, good_lse = pbs.tree_attn(q, t.k, t.v, t.table, i32([20, 5, 9], dev), lse=True)
+
+    def junk():  # what the allocator hands out next
+        for x in (q.shape, q.shape[:3]):
+            torch.full(x, 7, dtype=q.dtype if len(x) == 4 else FP32, device=dev)
+
+    for _ in range(3):
+        junk()
+        o, lse = pbs.tree_attn(q, t.k, t.v, t.table, start, lse=True)
+        assert pbs.device_status() == _lib.ERR_DEVICE_ASSERT
+        assert not o[[0, 2]].any() and not lse[[0, 2]].any()
+        assert torch.equal(o[1], good[1]) and torch.equal(lse[1], good_lse[1])
+    out = torch.full_like(q, 3)
+    junk()
+    _, lse = pbs.tree_attn(q, t.k, t.v, t.table, start, lse=True, out=out)
+    assert pbs.device_status() == _lib.ERR_DEVICE_ASSERT
+    assert (out[[0, 2]] == 3).all() and not lse[[0, 2]].any() and torch.equal(out[1], good[1])
