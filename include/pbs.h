@@ -600,7 +600,8 @@ pbs_status pbs_tree_mask(const int32_t *parents, uint32_t *mask, int32_t *depth,
  * set in mask row i (mask NULL: j <= i, a chain). With tree == 1 this is a
  * decoding step. Logits sigma * q . k, the softmax's maximum and sum and the
  * output's sums are fp32; the weights are rounded to 16 bits for the product
- * with V.
+ * with V: half a step of the type each, and those below 2^-32 of the largest
+ * may be lost in fp16.
  *
  *   q    [seqs, hq, tree, d] (layer stride unused), bf16 or fp16
  *   k_pages, v_pages [pages, hkv, page, d]: one layer (c.layers is ignored);

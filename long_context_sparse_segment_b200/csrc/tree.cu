@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(MmaCfg<D, W>::THREADS, MmaCfg<D, W>::CTAS)
                 if (!(seen >> (n * 8 + e) & 1)) s[n][2 * x + e] = -INFINITY;
           }
         }
-        // running maximum; P rounded to 16 bits (see tree.cuh)
+        // running reference (the maximum, or below it); P rounded to 16 bits (see
+        // tree.cuh)
         uint32_t p[4];
         float alpha[2];
 #pragma unroll
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(MmaCfg<D, W>::THREADS, MmaCfg<D, W>::CTAS)
           float t = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-          const float top = fmaxf(m[x], t * a.sl2);
+          const float top = fmaxf(m[x], reference<T>(t, a.sl2, 0.f));
           alpha[x] = part_scale(m[x], top);
           m[x] = top;
           const float mu = top == -INFINITY ? 0.f : top;

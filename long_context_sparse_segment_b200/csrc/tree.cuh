@@ -11,10 +11,15 @@
 // timing.
 //
 // The weights P are rounded to 16 bits for the product with V; their sum takes
-// the unrounded ones. A weight is off by half a step at most, independently
-// from key to key, so the output gains about as much error as its own rounding
-// has (1.4 times it together). A second 16-bit part would take that away: under
-// the power limit it cost 5 % of a decoding step and 10 % of 7 drafts over 128K.
+// the unrounded ones. They are taken relative to a reference: in bf16 the running
+// maximum; in fp16 a power of two below it (`reference`), since fp16 loses weights
+// below 2^-25 altogether: 131071 keys 2^25.1 below one of the same item would come
+// out 0.36 % short. So fp16 keeps weights down to 2^-40 of the maximum, or 2^-32
+// under the tcgen05 kernel's, which lags. A weight is off by half a step at most,
+// independently from key to key, so the output gains about as much error as its
+// own rounding has (1.4 times it together). A second 16-bit part would take that
+// away: under the power limit it cost 5 % of a decoding step and 10 % of 7 drafts
+// over 128K.
 #pragma once
 
 #include <cuda.h>
@@ -69,7 +74,7 @@ struct TreeArgs {
   void *out;
   float *lse;
   float4 *part_o;   // [2 grid][d / 4][rows]: neighbouring rows side by side
-  float2 *part_ml;  // [2 grid][rows]: running maximum (log2) and sum
+  float2 *part_ml;  // [2 grid][rows]: the weights' reference (log2) and sum
   int *part_bad;    // [2 grid]: drafted V rows with NaN or infinity met
   int2 *items;      // [seqs][hkv][tiles]: an item's first part, and its last CTA
   int *err;
@@ -261,6 +266,7 @@ template <>
 struct Two<__nv_bfloat16> {
   static __device__ __forceinline__ uint32_t pack(float x, float y) { return pack_bf16(x, y); }
   static constexpr uint32_t kExp = 0x7f80u;
+  static constexpr float kTop = 0.f;
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
     mma_16816(c, a, b0, b1);
@@ -273,6 +279,7 @@ struct Two<__half> {
     return *reinterpret_cast<const uint32_t *>(&v);
   }
   static constexpr uint32_t kExp = 0x7c00u;
+  static constexpr float kTop = 15.f;  // 2^15, the largest power of two below 65504
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
     asm volatile(
@@ -282,6 +289,20 @@ struct Two<__half> {
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 };
+
+// The reference of the weights under a maximum logit `s` (times sl2: log2) that
+// may rise by up to `lag` before it is moved: so far below that the largest
+// weight is 2^kTop. Rounded up, so that it is never more (fp16 has no room above).
+template <typename T>
+__device__ __forceinline__ float reference(float s, float sl2, float lag) {
+  return Two<T>::kTop == 0.f ? s * sl2 : __fmaf_ru(s, sl2, lag - Two<T>::kTop);
+}
+// How high the reference of a new maximum may lie before it replaces m; rounded
+// down for the same reason.
+template <typename T>
+__device__ __forceinline__ float may_rise(float m, float lag) {
+  return Two<T>::kTop == 0.f ? m + lag : __fadd_rd(m, lag);
+}
 
 // NaN or infinity in a 16-bit value.
 template <typename T>
@@ -355,7 +376,7 @@ __device__ __forceinline__ void write_lse(const TreeArgs &a, int s, int head, in
         l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// 2^(m - top) for a part whose maximum is m, top the maximum of all parts.
+// 2^(m - top) for a part whose reference is m, top the highest of all parts'.
 __device__ __forceinline__ float part_scale(float m, float top) {
   return m == top ? 1.f : ex2_approx(m - top);
 }

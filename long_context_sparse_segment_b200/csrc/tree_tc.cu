@@ -39,7 +39,7 @@ constexpr int kThreads = 384;
 // thread x 384 threads = 64512 = 128 x 56 + 256 x 224.
 constexpr int kLaunchRegs = 168, kCtrlRegs = 56, kSoftmaxRegs = 224;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split");
-constexpr float kRescaleLog2 = 8.f;  // the running maximum moves by more than 2^8 or not at all
+constexpr float kRescaleLog2 = 8.f;  // the weights' reference moves by more than 2^8 or not at all
 constexpr int kBadSlots = 8;         // segments in flight: at most VS + 2
 
 template <int D, bool PAIR>
@@ -462,9 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], __uint_as_float(v[c + e]));
       const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                              fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-      const float mxs = mx * a.sl2;
+      const float mxs = reference<T>(mx, a.sl2, kRescaleLog2);
       float alpha = 1.f;
-      if (mxs > m_used + kRescaleLog2) {
+      if (mxs > may_rise<T>(m_used, kRescaleLog2)) {
         alpha = ex2_approx(m_used - mxs);
         m_used = mxs;
       }

@@ -1,6 +1,7 @@
 """The decoding operators where their calls meet: inputs that are outputs, calls
 behind one that failed, sequences that a kernel refuses, and the far ends of
 types and lengths."""
+import math
 import random
 
 import pytest
@@ -149,3 +150,58 @@ def test_refused_sequences_are_zero_in_what_is_allocated(tree, dev):
     _, lse = pbs.tree_attn(q, t.k, t.v, t.table, start, lse=True, out=out)
     assert pbs.device_status() == _lib.ERR_DEVICE_ASSERT
     assert (out[[0, 2]] == 3).all() and not lse[[0, 2]].any() and torch.equal(out[1], good[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tree", [1, 8, 64])
+def test_fp16_keeps_small_weights(tree, d, dev):
+    """One key 2^25 above the 131071 others, which are 0.36 % of the softmax
+    together, in batches whose CTAs work through whole items (300 sequences on
+    the same pages). With the one's V row 0 the output is those 0.36 % alone. The
+    result rounds by half a step, the weights by half a step of theirs; an item
+    is summed in one, two (up to 128 rows), four or eight streams (16 rows: the
+    warps of a CTA, d = 64 or 128), where each product may be a step within 2^-23
+    of the sum so far (fp32, cut off: the tensor cores' sums need not round)."""
+    g, b, n, page = 4, 300, 131072 - tree, 64
+    pages = 131072 // page
+    k = torch.zeros(pages, 1, page, d, device=dev).half()
+    v = (0.5 + torch.rand(k.shape, generator=torch.Generator(dev).manual_seed(d), device=dev)).half()
+    table = torch.arange(pages, device=dev, dtype=torch.int32).expand(b, pages).contiguous()
+    q = torch.zeros(b, g, tree, d, device=dev).half()
+    q[..., 0] = 1
+    steps = 131072 / {1: d // 16, 8: 2, 64: 1}[tree] * 2.0 ** -23
+    for at in (3, n // 2, n - 70):
+        k.zero_()
+        k[at // page, 0, at % page, 0] = 25.1 * math.log(2)
+        e = k.view(-1, d)[:, 0].double().exp()
+        total = e.cumsum(0)[n:]
+        for alone in (False, True):
+            vv = v.clone()
+            if alone:
+                vv[at // page, 0, at % page] = 0
+            o, lse = pbs.tree_attn(q, k, vv, table, i32([n] * b, dev), scale=1.0, lse=True)
+            want = (e[:, None] * vv.view(-1, d).double()).cumsum(0)[n:] / total[:, None]
+            tol = 2.0 ** -11 * (2 if alone else 1.004) + steps
+            assert ((o.double() / want - 1).abs().max()) <= tol
+            assert ((lse.double() - total.log()).abs().max()) <= steps + 18 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("tree,g", [(1, 4), (8, 4), (64, 4)])
+def test_huge_logits_pick_the_largest(tree, g, dtype, dev):
+    """Logits of up to 3e8, where a step of fp32 is 32: every row is the V row
+    of its largest logit, and finite."""
+    d, n = 64, 700
+    k = torch.zeros(12, 2, 64, d, device=dev)
+    at = torch.randperm(n, generator=torch.Generator().manual_seed(tree))[:16].to(dev)
+    k[at // 64, :, at % 64, torch.arange(16, device=dev)] = 30.0
+    k, v = k.to(dtype), torch.randn(k.shape, device=dev).to(dtype)
+    pick = torch.randint(0, 16, (1, 2 * g, tree), device=dev)
+    q = torch.nn.functional.one_hot(pick, d).to(dtype) * 20
+    table = torch.arange(12, device=dev, dtype=torch.int32)[None]
+    for scale in (1e3, 1e5, 5e5):
+        o = pbs.tree_attn(q, k, v, table, i32([n], dev), scale=scale)
+        where = at[pick]
+        head = (torch.arange(2 * g, device=dev) // g)[None, :, None].expand_as(pick)
+        want = v[where // 64, head, where % 64]
+        assert ((o.float() - want.float()).abs() <= 2.0 ** -9 * want.float().abs()).all()
