@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(MmaCfg<D, W>::THREADS, MmaCfg<D, W>::CTAS)
     // pages behind it do not. The table is read 32 entries at a time, 32 early:
     // one entry a unit early held a unit to the latency of L2 (700 cycles, more
     // than the 64 keys of d = 64 take to arrive).
-    Walk<ROWS, kKeys> walk(place);
     Segment g;
+    Walk<ROWS, kKeys> walk(a, place, &g);
     const int kv = lane & 1, piece = lane >> 1, shift = 31 - __clz(a.page);
     const bool mine = piece < kKeys / box;
     int it = 0, seg = 0;
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(MmaCfg<D, W>::THREADS, MmaCfg<D, W>::CTAS)
       int t = g.k0 * kKeys + piece * box;
       const int last = (min(len, g.k1 * kKeys) - 1) >> shift;  // column
       int col = g.k0 * kKeys >> shift;                         // of lane 0's entry
-      auto entry = [&](int c) { return c + lane <= last ? __ldg(row + c + lane) : 0; };
+      auto entry = [&](int c) { return c + lane <= last ? row[c + lane] : 0; };
       int held = entry(col), ahead = entry(col + 32);
       for (int k = g.k0; k < g.k1; ++k, ++it, t += kKeys) {
         const int st = it % ST;

@@ -37,7 +37,10 @@ using namespace tc;
 // Programmatic dependent launch. The kernels of a call are launched while the
 // kernel in front of them may still run, set themselves up, and wait for its end
 // before they read or write anything that another kernel knows: 1 to 2 us a call.
-// Every block waits, so that a kernel never ends before the one in front.
+// Every block waits, so that a kernel never ends before the one in front. Nothing is
+// read through the read-only path (__ldg, ld.global.nc), which is for memory that
+// nobody writes while the kernel is in flight and need not stay behind the wait:
+// the kernel in front may still write the lengths, tables and masks.
 
 // Allows the kernel launched behind this one to start.
 __device__ __forceinline__ void allow_next() {
@@ -86,19 +89,31 @@ struct TreeArgs {
 };
 
 // What a sequence asks for: its cached tokens and drafts (0 where the call
-// has to leave it alone).
+// has to leave it alone, which the joining kernel reports).
 struct Seq {
   int start, count;
 };
 
-__device__ __forceinline__ Seq seq_of(const TreeArgs &a, int s) {
-  Seq q{__ldg(a.start + s), a.count ? min(__ldg(a.count + s), a.tree) : a.tree};
-  if (q.count <= 0) return {0, 0};
-  if (q.start < 0 || (int64_t)q.start + q.count > (int64_t)a.width * a.page) {
-    report(a.err, PBS_ERR_DEVICE_ASSERT);
+// Its lengths as they stand in memory; 0 behind the last sequence.
+__device__ __forceinline__ Seq read_seq(const TreeArgs &a, int s) {
+  if (s >= a.seqs) return {0, 0};
+  return {a.start[s], a.count ? a.count[s] : a.tree};
+}
+// They will be read soon (held in registers from here on instead, they cost the
+// tcgen05 kernel more in spills: 7 drafts over 128K tokens 93.6 us, so 92.7).
+__device__ __forceinline__ void touch_seq(const TreeArgs &a, int s) {
+  if (s >= a.seqs) return;
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(a.start + s));
+  if (a.count) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.count + s));
+}
+__device__ __forceinline__ Seq check_seq(const TreeArgs &a, Seq q) {
+  q.count = min(q.count, a.tree);
+  if (q.count <= 0 || q.start < 0 || (int64_t)q.start + q.count > (int64_t)a.width * a.page)
     return {0, 0};
-  }
   return q;
+}
+__device__ __forceinline__ Seq seq_of(const TreeArgs &a, int s) {
+  return check_seq(a, read_seq(a, s));
 }
 
 __device__ __forceinline__ int cdiv(int x, int y) { return (x + y - 1) / y; }
@@ -136,9 +151,10 @@ struct Runs {
 };
 
 // The place of a CTA's run: its first and end unit, and the sequence that the
-// first lies in with the units before that one.
+// first lies in with what it asks for and the units before it.
 struct Place {
   int u0, u1, s, before;
+  Seq q;
   Runs run;
 };
 
@@ -147,29 +163,31 @@ struct Place {
 template <int ROWS, int KEYS, int NT>
 __device__ __forceinline__ bool find_place(const TreeArgs &a, int *sum, Place *p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto units = [&](int s) { return s < a.seqs ? units_of<ROWS, KEYS>(a, seq_of(a, s)) : 0; };
   // up to 32 sequences a warp holds them all and nobody waits for another; more
   // are summed by the block first (a barrier and a second look at the lengths)
-  int x = units(a.seqs <= 32 ? lane : tid), total = x;
+  Seq ahead = read_seq(a, lane);  // of the next 32 sequences
+  int total = 0;
   if (a.seqs > 32) {
-    for (int s = tid + NT; s < a.seqs; s += NT) total += units(s);
+    for (int s = tid; s < a.seqs; s += NT) total += units_of<ROWS, KEYS>(a, seq_of(a, s));
     total = __reduce_add_sync(0xffffffffu, total);
     if (lane == 0) sum[warp] = total;
     __syncthreads();
     total = 0;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) total += sum[w];
-    x = units(lane);
   } else {
-    total = __reduce_add_sync(0xffffffffu, total);
+    total = __reduce_add_sync(0xffffffffu, units_of<ROWS, KEYS>(a, check_seq(a, ahead)));
   }
   const int runs = min(total, (int)gridDim.x);
   if ((int)blockIdx.x >= runs) return false;
   const Runs run(total, runs);
   p->u0 = run.start(blockIdx.x), p->u1 = run.start(blockIdx.x + 1), p->run = run;
   int base = 0;
+#pragma unroll 1
   for (int s0 = 0; s0 < a.seqs; s0 += 32) {
-    if (s0 > 0) x = units(s0 + lane);
+    const Seq q = check_seq(a, ahead);
+    ahead = read_seq(a, s0 + 32 + lane);
+    const int x = units_of<ROWS, KEYS>(a, q);
     int inc = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -181,6 +199,7 @@ __device__ __forceinline__ bool find_place(const TreeArgs &a, int *sum, Place *p
     if (m) {
       const int l = __ffs(m) - 1;
       p->s = s0 + l, p->before = __shfl_sync(0xffffffffu, inc - x, l);
+      p->q = Seq{__shfl_sync(0xffffffffu, q.start, l), __shfl_sync(0xffffffffu, q.count, l)};
       return true;
     }
     base = __shfl_sync(0xffffffffu, inc, 31);
@@ -206,25 +225,30 @@ __device__ __forceinline__ void tell_item(const TreeArgs &a, const Segment &g, c
         make_int2(slot, g.whole ? (int)blockIdx.x : run.owner(g.last));
 }
 
-// The segments of a run, one after the other.
+// The segments of a run, one after the other. A sequence's lengths are read when
+// the walk comes to it; the segment holds them from one call to the next.
 template <int ROWS, int KEYS>
 struct Walk {
   int u, u1, s, before;
-  __device__ __forceinline__ explicit Walk(const Place &p)
-      : u(p.u0), u1(p.u1), s(p.s), before(p.before) {}
+  __device__ __forceinline__ Walk(const TreeArgs &a, const Place &p, Segment *g)
+      : u(p.u0), u1(p.u1), s(p.s), before(p.before) {
+    g->start = p.q.start, g->count = p.q.count;
+    touch_seq(a, s + 1);
+  }
   __device__ __forceinline__ bool next(const TreeArgs &a, Segment *g) {
     while (u < u1) {
-      Seq q = seq_of(a, s);
+      Seq q{g->start, g->count};
       for (int n; u >= before + (n = units_of<ROWS, KEYS>(a, q));) {
         before += n;
         if (++s >= a.seqs) return false;  // the lengths changed under this call
         q = seq_of(a, s);
+        touch_seq(a, s + 1);
       }
+      g->start = q.start, g->count = q.count;
       constexpr int X = kExtra<ROWS>;
       const int kt = cdiv(q.start + q.count, KEYS), rts = cdiv(q.count * a.G, ROWS);
       const int x = u - before, item = x / (kt + X), at = x - item * (kt + X) - X;
       g->s = s, g->h = item / rts, g->rt = item - g->h * rts;
-      g->start = q.start, g->count = q.count;
       g->k0 = max(at, 0);
       g->k1 = min(kt, at + u1 - u);
       g->whole = g->k1 - g->k0 == kt;
@@ -239,7 +263,7 @@ struct Walk {
 // Whether draft i sees draft j (j < count).
 __device__ __forceinline__ bool sees(const TreeArgs &a, int s, int i, int j) {
   if (!a.mask) return j <= i;
-  return __ldg(a.mask + ((size_t)s * a.tree + i) * a.words + (j >> 5)) >> (j & 31) & 1;
+  return a.mask[((size_t)s * a.tree + i) * a.words + (j >> 5)] >> (j & 31) & 1;
 }
 
 // Bit x of the result: whether draft i of sequence s sees key `key` + x, given
@@ -250,7 +274,7 @@ __device__ __forceinline__ uint32_t seen_word(const TreeArgs &a, const Segment &
   auto word = [&](int w) -> uint32_t {
     if (w < 0) return 0xffffffffu;  // the prefix
     if (w >= a.words) return 0;
-    if (a.mask) return __ldg(a.mask + ((size_t)g.s * a.tree + i) * a.words + w);
+    if (a.mask) return a.mask[((size_t)g.s * a.tree + i) * a.words + w];
     return w < i >> 5 ? 0xffffffffu : w > i >> 5 ? 0u : (2u << (i & 31)) - 1;
   };
   const int w = j >> 5;
@@ -338,7 +362,7 @@ __device__ __noinline__ void add_wild(const TreeArgs &a, int s, int h, const Seq
   for (int j = 0; j < q.count; ++j) {
     if (!sees(a, s, i, j)) continue;
     const int t = q.start + j;
-    const int page = __ldg(a.table + (size_t)s * a.width + t / a.page);
+    const int page = a.table[(size_t)s * a.width + t / a.page];
     if (page < 0 || page >= a.pages) continue;
     const T *v = (const T *)a.v_pages +
                  (((size_t)page * a.hkv + h) * a.page + t % a.page) * d + col;
@@ -419,7 +443,8 @@ __global__ void __launch_bounds__(kCombineThreads)
   const int first = blockIdx.x * heads;
   const int pair = MANY ? min(first + lane, a.seqs * a.hkv - 1) : 0;
   // the attention kernel has not changed the lengths
-  const Seq own = seq_of(a, MANY ? pair / a.hkv : blockIdx.z);
+  const Seq asked = read_seq(a, MANY ? pair / a.hkv : blockIdx.z), own = check_seq(a, asked);
+  if (asked.count > 0 && own.count == 0) report(a.err, PBS_ERR_DEVICE_ASSERT);
   wait_previous();
   unsigned todo = 1;
   if constexpr (MANY) {

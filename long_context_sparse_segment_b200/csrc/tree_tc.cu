@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) sh->place = place;
   }
   __syncthreads();
-  Walk<ROWS, kTile> walk(sh->place);
   Segment g{};
+  Walk<ROWS, kTile> walk(a, sh->place, &g);
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
     if (warp == 0) {
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t *row = a.table + (size_t)g.s * a.width;
         auto page_of = [&](int k) {
           const int t = k * kTile + piece * box;
-          return mine && k < g.k1 && t < len ? __ldg(row + (t >> shift)) : -1;
+          return mine && k < g.k1 && t < len ? row[t >> shift] : -1;
         };
         auto row_of = [&](int k, int page) {
           const int t = k * kTile + piece * box;
@@ -425,6 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int draft = min((g.rt * ROWS + row) / a.G, g.count - 1);
     float m_used = -INFINITY, l = 0.f;
     for (int j = 0; j < steps; ++j) {
+      const int key = (g.k0 + (PAIR ? j : 2 * j + x)) * kTile;
+      // the masks' words are on their way while S is computed
+      const bool edge = key + kTile > g.start;
+      uint32_t seen[4];
+      if (edge && live) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) seen[c] = seen_word(a, g, draft, key + 32 * c);
+      }
       if (!mbar_wait_warp(&sh->s_full[x], s_phase, abort, a.err, 41)) {
         ok = false;
         break;
@@ -437,21 +445,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(&sh->p_full[x][1], lane);
         continue;
       }
-      const int key = (g.k0 + (PAIR ? j : 2 * j + x)) * kTile;
       uint32_t v[kTile];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < kTile; ++c) asm volatile("" : "+r"(v[c]));
-      if (key + kTile > g.start) {
+      if (edge) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t seen = seen_word(a, g, draft, key + 32 * c);
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (!(seen >> e & 1)) v[c * 32 + e] = 0xff800000u;  // -inf
-        }
+            if (!(seen[c] >> e & 1)) v[c * 32 + e] = 0xff800000u;  // -inf
       }
       float m8[8];
 #pragma unroll

@@ -1,6 +1,8 @@
 """Host side of the decoding operators: what the C ABI and the binding refuse
 beyond test_decode.py. Nothing here reaches a kernel."""
 import ctypes
+import pathlib
+import re
 
 import pytest
 
@@ -31,3 +33,17 @@ def test_accepted_lengths_inside_another_input_are_refused(lens, refs):
     assert pbs.lib().pbs_cache_accept(
         at(1 << 16), at(1 << 18), at(1 << 14), at(0), at(1 << 13), None, at(lens), 3, c,
         None) == _lib.ERR_INVALID_ARG
+
+
+def test_kernels_launched_early_read_nothing_as_read_only():
+    """Kernels that start while the one in front may still write their inputs
+    wait for its end; loads of the read-only path need not stay behind that."""
+    csrc = pathlib.Path(_lib.LIB_PATH).parent / "csrc"
+    for f in ("tree.cuh", "tree.cu", "tree_tc.cu"):
+        code = re.sub(r"//[^\n]*", "", (csrc / f).read_text())
+        assert "__ldg" not in code and "global.nc" not in code and "__ldcs" not in code, f
+    # the compaction's copies, the one such kernel of cache.cu
+    code = (csrc / "cache.cu").read_text()
+    kernel = code[code.index("copy_kernel(uint4"):code.index("append, accept")]
+    assert "griddepcontrol.wait" in kernel
+    assert "__ldg" not in kernel and "__restrict__" not in kernel
