@@ -454,7 +454,8 @@ typedef enum { PBS_BF16 = 0, PBS_FP16 = 1, PBS_FP32 = 2 } pbs_dtype;
  * element is rounded once.
  *
  *   q, q_out  [batch, hq, n, d]  (layer stride unused); q_out may be q and
- *             k_out k, rows and all, and no output overlaps anything else
+ *             k_out k, rows and all, and no output overlaps anything else:
+ *             refused (slices of one buffer may interleave)
  *   k, k_out  [batch, hkv, n, d] or k.p == NULL with hkv == 0
  *   pos       int32, pos[b * pos_batch + i] (pos_batch 0: one row for all)
  *   inv_freq  [rot/2] fp64, radians per position
@@ -613,8 +614,9 @@ pbs_status pbs_tree_mask(const int32_t *parents, uint32_t *mask, int32_t *depth,
  *        their lse too.
  * A token that a row does not see has no part in it, whatever its K and V
  * hold (NaN and infinities too). The workspace belongs to one call at a time:
- * calls that may overlap on the GPU need one each. The lengths, tables and
- * masks may not change while the call runs.
+ * calls that may overlap on the GPU need one each. out, lse and the workspace
+ * overlap nothing: refused. The lengths, tables and masks may not change while
+ * the call runs.
  */
 pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
                          const int32_t *table, const int32_t *start, const int32_t *count,

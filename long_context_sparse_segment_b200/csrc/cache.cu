@@ -491,11 +491,6 @@ __global__ void __launch_bounds__(kAcceptThreads)
   if (!__syncthreads_or(bad) && threadIdx.x == 0) lens[s] = st + max(n, 0);
 }
 
-// Whether [a, a + an) and [b, b + bn) meet; a null one meets nothing.
-bool meet(const void *a, size_t an, const void *b, size_t bn) {
-  return a && b && (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
-}
-
 bool cache_ok(const pbs_cache &c) {
   return c.layers >= 1 && c.pages >= 1 && c.hkv >= 1 && c.page >= 1 && c.d >= 8 && c.d % 8 == 0 &&
          c.seqs >= 0 && c.width >= 1 && c.pages < (1 << 30) && c.hkv <= 65536 &&
@@ -650,10 +645,11 @@ pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,
       (c.refs && !ints_ok(c.refs)))
     return PBS_ERR_INVALID_ARG;
   // lens may be start or count, but otherwise nothing that other sequences read
-  const size_t each = 4 * (size_t)c.seqs;
-  if ((lens != start && meet(lens, each, start, each)) ||
-      (lens != count && meet(lens, each, count, each)) || meet(lens, each, path, each * tree) ||
-      meet(lens, each, table, each * c.width) || meet(lens, each, c.refs, 4 * (size_t)c.pages))
+  const int64_t each = 4ll * c.seqs;
+  if ((lens != start && bytes_meet(lens, each, start, each)) ||
+      (lens != count && bytes_meet(lens, each, count, each)) ||
+      bytes_meet(lens, each, path, each * tree) || bytes_meet(lens, each, table, each * c.width) ||
+      bytes_meet(lens, each, c.refs, 4ll * c.pages))
     return PBS_ERR_INVALID_ARG;
   const int col_blocks = (int)ceil_div((int64_t)c.hkv * (c.d / 8), kAcceptThreads);
   const int64_t gx = 2LL * c.layers * col_blocks;

@@ -21,6 +21,31 @@ inline bool rows_ok(const pbs_rows &r, int elem) {
          r.head % v == 0 && r.row % v == 0;
 }
 
+// Whether [a, a + an) and [b, b + bn) meet; a null one meets nothing.
+inline bool bytes_meet(const void *a, int64_t an, const void *b, int64_t bn) {
+  return a && b && an > 0 && bn > 0 && (uintptr_t)a < (uintptr_t)b + (uintptr_t)bn &&
+         (uintptr_t)b < (uintptr_t)a + (uintptr_t)an;
+}
+
+// Rows [batch, heads, n, d] of `elem` bytes an element.
+struct RowSet {
+  pbs_rows r;
+  int64_t batch, heads, n;
+  int d, elem;
+  // elements from the first one to behind the last
+  int64_t span() const {
+    return r.batch * (batch - 1) + r.head * (heads - 1) + r.row * (n - 1) + d;
+  }
+  bool plain() const { return r.batch >= 0 && r.head >= 0 && r.row >= 0; }
+  bool empty() const { return batch <= 0 || heads <= 0 || n <= 0 || d <= 0; }
+};
+
+// Whether two sets of rows share memory: element by element where their strides
+// are equal (slices of one buffer, which may interleave), else by their spans.
+bool rows_meet(const RowSet &x, const RowSet &y);
+// ... and whether a set of rows and some bytes do, by the span.
+bool rows_meet(const RowSet &x, const void *p, int64_t bytes);
+
 // SMs of the current device, looked up once per device.
 int sm_count_cached();
 

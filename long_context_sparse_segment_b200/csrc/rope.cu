@@ -170,7 +170,56 @@ void launch(const RopeArgs &a, dim3 grid, bool half, cudaStream_t st) {
     rope_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
 }
 
+// Whether some i < n, j < m of every dimension have sum (i - j) s = off, up to
+// less than d elements; `dims` by falling stride.
+struct MeetDim {
+  int64_t s, n, m;
+};
+bool dims_meet(const MeetDim *dims, int k, int64_t off, int d) {
+  if (k == 0) return off < d && -off < d;
+  int64_t rest = d - 1;
+  for (int i = 1; i < k; ++i)
+    rest += dims[i].s * ((dims[i].n > dims[i].m ? dims[i].n : dims[i].m) - 1);
+  // |off - t s| <= rest, -m < t < n
+  auto down = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+  int64_t lo = -down(rest - off, dims->s), hi = down(off + rest, dims->s);
+  if (lo < 1 - dims->m) lo = 1 - dims->m;
+  if (hi > dims->n - 1) hi = dims->n - 1;
+  if (hi - lo > 3) return true;  // strides that reach into one another: taken to meet
+  for (int64_t t = lo; t <= hi; ++t)
+    if (dims_meet(dims + 1, k - 1, off - t * dims->s, d)) return true;
+  return false;
+}
+
 }  // namespace
+
+bool rows_meet(const RowSet &x, const void *p, int64_t bytes) {
+  if (x.empty()) return false;
+  return !x.plain() || bytes_meet(x.r.p, x.span() * x.elem, p, bytes);
+}
+
+bool rows_meet(const RowSet &x, const RowSet &y) {
+  if (x.empty() || y.empty()) return false;
+  if (!x.plain() || !y.plain()) return true;
+  if (!bytes_meet(x.r.p, x.span() * x.elem, y.r.p, y.span() * y.elem)) return false;
+  const int64_t bytes = (intptr_t)y.r.p - (intptr_t)x.r.p;
+  if (x.elem != y.elem || x.d != y.d || bytes % x.elem) return true;
+  const int64_t s[2][3] = {{x.r.batch, x.r.head, x.r.row}, {y.r.batch, y.r.head, y.r.row}};
+  const int64_t n[2][3] = {{x.batch, x.heads, x.n}, {y.batch, y.heads, y.n}};
+  MeetDim dims[3];
+  int k = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (n[0][i] == 1 && n[1][i] == 1) continue;
+    const int64_t st = n[0][i] == 1 ? s[1][i] : s[0][i];
+    if (n[0][i] > 1 && n[1][i] > 1 && s[0][i] != s[1][i]) return true;
+    if (st == 0) continue;
+    int at = k++;
+    for (; at > 0 && dims[at - 1].s < st; --at) dims[at] = dims[at - 1];
+    dims[at] = {st, n[0][i], n[1][i]};
+  }
+  return dims_meet(dims, k, bytes / x.elem, x.d);
+}
+
 }  // namespace pbs
 
 using namespace pbs;
@@ -189,6 +238,22 @@ extern "C" pbs_status pbs_rope(pbs_rows q, pbs_rows q_out, int hq, pbs_rows k, p
       (hkv > 0 && (!rows_ok(k, elem) || !rows_ok(k_out, elem))) || !pos ||
       ((uintptr_t)pos & 3u) || (rot > 0 && (!inv_freq || ((uintptr_t)inv_freq & 7u))))
     return PBS_ERR_INVALID_ARG;
+  // an output may be its own input, rows and all, and otherwise meets nothing
+  const RowSet sets[4] = {{q, batch, hq, n, d, elem},
+                          {k, batch, hkv, n, d, elem},
+                          {q_out, batch, hq, n, d, elem},
+                          {k_out, batch, hkv, n, d, elem}};
+  const int64_t pos_bytes = 4 * ((pos_batch < 0 ? -pos_batch : pos_batch) * (batch - 1) + n);
+  for (int o = 2; o < 4; ++o) {
+    for (int i = 0; i < o; ++i) {
+      const pbs_rows &x = sets[i].r, &y = sets[o].r;
+      const bool own = i == o - 2 && x.p == y.p && (batch == 1 || x.batch == y.batch) &&
+                       (sets[i].heads == 1 || x.head == y.head) && (n == 1 || x.row == y.row);
+      if (!own && rows_meet(sets[i], sets[o])) return PBS_ERR_INVALID_ARG;
+    }
+    if (rows_meet(sets[o], pos, pos_bytes) || rows_meet(sets[o], inv_freq, 4ll * rot))
+      return PBS_ERR_INVALID_ARG;
+  }
   RopeArgs a{q, q_out, k, k_out, pos, inv_freq, pos_batch, (int64_t)batch * n, gain};
   a.hq = hq, a.heads = hq + hkv, a.n = n, a.d = d, a.rot = rot, a.transpose = transpose != 0;
   const int64_t bx = ceil_div(a.tokens * (d * elem / 32), kThreads);

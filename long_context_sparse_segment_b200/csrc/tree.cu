@@ -585,6 +585,20 @@ pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,
   const int rows = row_tile(hq, tree, c);
   const Parts p = parts(rows, hq, tree, c);
   if (ws_bytes < p.bytes) return PBS_ERR_WORKSPACE;
+  // what is written meets nothing else
+  {
+    const int64_t some = (int64_t)c.seqs * hq * tree, pool = 2ll * c.pages * c.hkv * c.page * c.d;
+    const pbs_rows dense{out, 0, (int64_t)hq * tree * c.d, (int64_t)tree * c.d, c.d};
+    const RowSet qs{q, c.seqs, hq, tree, c.d, 2}, os{dense, c.seqs, hq, tree, c.d, 2};
+    const void *ptr[] = {out, lse, ws, k_pages, v_pages, table, start, count, mask};
+    const int64_t len[] = {some * c.d * 2, some * 4, (int64_t)p.bytes, pool, pool,
+                           4ll * c.seqs * c.width, 4ll * c.seqs, 4ll * c.seqs,
+                           4ll * c.seqs * tree * ((tree + 31) / 32)};
+    bool meet = rows_meet(qs, os) || rows_meet(qs, lse, len[1]) || rows_meet(qs, ws, len[2]);
+    for (int o = 0; o < 3; ++o)
+      for (int i = o + 1; i < 9; ++i) meet |= bytes_meet(ptr[o], len[o], ptr[i], len[i]);
+    if (meet) return PBS_ERR_INVALID_ARG;
+  }
   TreeArgs a{};
   a.q = q, a.table = table, a.start = start, a.count = count, a.mask = mask, a.v_pages = v_pages;
   a.out = out, a.lse = lse;

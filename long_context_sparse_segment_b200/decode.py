@@ -101,19 +101,52 @@ def _rows(t, name, written=False):
 
 def _span(t):
     """The bytes from a tensor's first element to behind its last."""
+    p, size = t.data_ptr(), t.element_size()
+    if t.is_contiguous():
+        return p, p + t.numel() * size
     last = sum(st * (n - 1) for st, n in zip(t.stride(), t.shape))
-    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    return p, p + (last + 1) * size
+
+
+def _meet(x, y):
+    """Whether two tensors share memory. Slices of one buffer (equal strides) are
+    compared element by element, so that interleaved ones are apart; others by
+    their spans."""
+    if not (x.numel() and y.numel()):
+        return False
+    (a, b), (c, d) = _span(x), _span(y)
+    if b <= c or d <= a:
+        return False
+    size = x.element_size()
+    if x.dim() != y.dim() or y.element_size() != size or (c - a) % size:
+        return True
+    dims = []
+    for n, m, s, t in zip(x.shape, y.shape, x.stride(), y.stride()):
+        s, t = (t, t) if n == 1 else (s, s) if m == 1 else (s, t)
+        if s != t:
+            return True
+        if s and (n > 1 or m > 1):
+            dims.append((s, n, m))
+    dims.sort(reverse=True)
+
+    def hits(k, off):
+        """Whether sum_k (i - j) s = off for some i < n, j < m of dims[k:]."""
+        if k == len(dims):
+            return off == 0
+        s, n, m = dims[k]
+        rest = sum(st * (max(u, w) - 1) for st, u, w in dims[k + 1:])
+        lo, hi = max(-((rest - off) // s), 1 - m), min((off + rest) // s, n - 1)
+        return hi - lo > 3 or any(hits(k + 1, off - t * s) for t in range(lo, hi + 1))
+
+    return hits(0, (c - a) // size)
 
 
 def _apart(out, name, *others):
-    """An output that a call was given may not reach into its inputs."""
-    if out.numel():
-        a, b = _span(out)
-        for x in others:
-            if x.numel():
-                c, d = _span(x)
-                if a < d and c < b:
-                    raise ValueError(f"{name} overlaps an input")
+    """An output that a call was given may not reach into its inputs (the C call
+    looks at the other pairs)."""
+    for x in others:
+        if _meet(out, x):
+            raise ValueError(f"{name} overlaps an input")
 
 
 def rope_freqs(rot, base=10000.0, scaling=None, device=None):

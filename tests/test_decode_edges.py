@@ -1,14 +1,17 @@
 """Host side of the decoding operators: what the C ABI and the binding refuse
 beyond test_decode.py. Nothing here reaches a kernel."""
 import ctypes
+import itertools
 import pathlib
+import random
 import re
 
 import pytest
+import torch
 
 import long_context_sparse_segment_b200 as pbs
 from long_context_sparse_segment_b200 import _lib
-from test_decode import FAKE, cache, rows
+from test_decode import FAKE, cache, call_rope, call_tree, rows
 
 
 def at(x):
@@ -47,3 +50,60 @@ def test_kernels_launched_early_read_nothing_as_read_only():
     kernel = code[code.index("copy_kernel(uint4"):code.index("append, accept")]
     assert "griddepcontrol.wait" in kernel
     assert "__ldg" not in kernel and "__restrict__" not in kernel
+
+
+def shares(x, y):
+    """Whether two views of one buffer name a common element."""
+    at = lambda t: {t.storage_offset() + sum(i * s for i, s in zip(ix, t.stride()))
+                    for ix in itertools.product(*map(range, t.shape))}
+    return bool(at(x) & at(y))
+
+
+def test_overlaps_of_strided_tensors():
+    """Slices of one buffer against their elements one by one."""
+    from long_context_sparse_segment_b200.decode import _meet
+    base = torch.zeros(2, 5, 12, 8, dtype=torch.bfloat16)
+    buf = base.transpose(1, 2)
+    cuts = [buf[:, a:b] for a, b in ((0, 4), (4, 6), (3, 5), (6, 12), (0, 12), (5, 6))]
+    cuts += [buf[:, 4:8, 1:3], buf[:, 4:8, 3:], buf[:1, 2:9], buf[1:, 2:9], buf[..., :4],
+             buf[..., 4:], buf[:, 0:12:2], buf[:, 1:12:2], buf[:, :0], base,
+             base[:, :, :1].expand(2, 5, 12, 8), base.view(2, 5, 24, 4)[:, :, ::2]]
+    seen = set()
+    for x, y in itertools.product(cuts, cuts):
+        if x.stride() == y.stride() or not _meet(x, y):
+            assert _meet(x, y) == shares(x, y), (x.shape, x.stride(), y.shape, y.stride())
+            seen.add(_meet(x, y))
+    assert seen == {True, False}
+    # other strides and other types: by spans
+    assert _meet(base, base.view(torch.int32)) and not _meet(base, torch.zeros_like(base))
+    assert not _meet(base[:1], base.view(torch.uint8)[1:])
+    flat = torch.zeros(4096, dtype=torch.bfloat16)
+    rng = random.Random(0)
+    for _ in range(300):
+        st = (rng.choice([512, 64, 520]), rng.choice([64, 16, 128]), rng.choice([16, 8, 256]), 1)
+        view = lambda: flat.as_strided((rng.randint(1, 3), rng.randint(1, 4), rng.randint(1, 3),
+                                        rng.choice([4, 8])), st, rng.randrange(0, 1200, 4))
+        x, y = view(), view()
+        # nothing that overlaps is taken for apart, and the other way where no
+        # dimension reaches into another
+        if shares(x, y):
+            assert _meet(x, y)
+        elif st in ((512, 64, 16, 1), (512, 128, 16, 1), (512, 64, 8, 1)):
+            assert not _meet(x, y)
+
+
+def test_written_rows_that_meet_other_memory_are_refused():
+    """The same rows for everything; one output over the other input; over the
+    positions; a workspace over the table."""
+    r, far = rows(), rows(p=1 << 30)
+    for kw in (dict(), dict(q=far), dict(k=far, q=rows(p=1 << 32), ko=rows(p=1 << 34)),
+               dict(q=far, k=rows(p=1 << 32), ko=rows(p=1 << 34)),
+               dict(q=far, k=far, qo=rows(p=1 << 32), ko=rows(p=(1 << 32) + 64)),
+               dict(q=rows(batch=2048), qo=rows(batch=2056), k=far, ko=rows(p=1 << 32))):
+        assert call_rope(**kw) == _lib.ERR_INVALID_ARG
+    apart = [ctypes.c_void_p(1 << x) for x in range(25, 33)]
+    for i, name in enumerate(("k", "v", "table", "start", "count", "mask", "out", "lse")):
+        p = list(apart)
+        p[i] = FAKE  # the workspace's place
+        assert call_tree(cache(), ptrs=p, q=rows(p=1 << 40)) == _lib.ERR_INVALID_ARG, name
+    assert call_tree(cache(), ptrs=apart, q=rows(p=1 << 31)) == _lib.ERR_INVALID_ARG  # q is out

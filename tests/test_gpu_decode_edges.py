@@ -125,6 +125,86 @@ def test_nothing_is_written_into_shared_pages_behind_a_failed_reserve(whole, dev
     assert torch.equal(bits(c.k)[0, mine, :, 2:12], bits(new)[0, 1])
 
 
+# ------------------------------------------------------------------------ rope
+def test_rope_outputs_beside_and_over_other_tensors(dev):
+    """Head slices of one buffer: outputs that interleave with the inputs are
+    taken, in place too; outputs that reach into an input or into one another
+    are refused."""
+    b, n, d = 2, 5, 64
+    f = pbs.rope_freqs(d)[0].to(dev)
+    pos = torch.arange(n, dtype=torch.int32, device=dev)
+    buf = torch.randn(b, n, 12, d, device=dev).to(BF16).transpose(1, 2)
+    q, k, rest = buf[:, :4], buf[:, 4:6], buf[:, 6:]
+    want = pbs.rope(q, k, pos, f)
+    before = buf.clone()
+    got = pbs.rope(q, k, pos, f, q_out=rest[:, :4], k_out=rest[:, 4:])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(buf[:, :6], before[:, :6])
+    assert torch.equal(rest[:, :4], want[0]) and torch.equal(rest[:, 4:], want[1])
+    after = buf.clone()
+    for kw in (dict(q_out=buf[:, 2:6]), dict(q_out=buf[:, 5:9]), dict(k_out=buf[:, 3:5]),
+               dict(k_out=buf[:, 0:2]), dict(q_out=q, k_out=buf[:, 2:4]),
+               dict(q_out=buf[:, 5:9], k_out=k), dict(q_out=rest[:, :4], k_out=rest[:, 3:5])):
+        with pytest.raises((ValueError, pbs.PbsError)):
+            pbs.rope(q, k, pos, f, **kw)
+    with pytest.raises(pbs.PbsError):  # q and k the same rows, both turned in place
+        pbs.rope(q, q[:, :2], pos, f, q_out=q, k_out=q[:, :2])
+    assert torch.equal(buf, after)
+    pbs.rope(q, k, pos, f, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(rest, after[:, 6:])
+
+
+def test_rope_takes_just_the_outputs_that_are_apart(dev):
+    """Random slices of one buffer as inputs and outputs, against their elements
+    one by one."""
+    r = random.Random(5)
+    d = 16
+    f = pbs.rope_freqs(d)[0].to(dev)
+    base = torch.zeros(2 * 4 * 6 * d, dtype=FP32, device=dev)
+    names = torch.arange(base.numel()).view(2, 4, 6, d)
+    taken = 0
+    for turn in range(400):
+        layout = r.choice([(0, 2, 1, 3), (0, 1, 2, 3), (1, 0, 2, 3), (2, 0, 1, 3)])
+        buf, num = base.view(2, 4, 6, d).permute(layout), names.permute(layout)
+        size = [r.randint(1, buf.shape[0]), 0, r.randint(1, buf.shape[2])]
+        hq, hkv = (r.randint(1, max(1, buf.shape[1] // 2)) for _ in range(2))
+
+        def cut(h):
+            b, n = size[0], size[2]
+            at = [r.randint(0, x - y) for x, y in zip(buf.shape, (b, h, n))]
+            return tuple(slice(a, a + y) for a, y in zip(at, (b, h, n)))
+
+        q, k = cut(hq), cut(hkv)
+        qo, ko = (x if r.random() < 0.3 else cut(h) for x, h in ((q, hq), (k, hkv)))
+        if r.random() < 0.2:
+            ko = None
+        ids = {n: set(num[x].flatten().tolist()) for n, x in
+               dict(q=q, k=k, qo=qo, ko=ko).items() if x is not None}
+        bad = ids["qo"] & ids["k"] or (qo != q and ids["qo"] & ids["q"])
+        if ko is not None:
+            bad = bad or ids["ko"] & ids["q"] or ids["ko"] & ids["qo"] or \
+                (ko != k and ids["ko"] & ids["k"])
+        base.copy_(torch.randn(base.shape, generator=torch.Generator().manual_seed(turn)))
+        before = base.clone()
+        pos = torch.randint(0, 1000, (size[0], size[2]), dtype=torch.int32).to(dev)
+        call = lambda **kw: pbs.rope(buf[q], buf[k], pos, f, **kw)
+        want = call()
+        kw = dict(q_out=buf[qo], **({} if ko is None else dict(k_out=buf[ko])))
+        if bad:
+            with pytest.raises((ValueError, pbs.PbsError)):
+                call(**kw)
+            assert torch.equal(base, before)
+        else:
+            got = call(**kw)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            written = ids["qo"] | ids.get("ko", set())
+            rest = torch.ones(base.numel(), dtype=torch.bool)
+            rest[list(written)] = False
+            assert torch.equal(base[rest.to(dev)], before[rest.to(dev)])
+            taken += 1
+    assert 100 < taken < 300
+
+
 # ------------------------------------------------------------------- attention
 @pytest.mark.parametrize("tree", [1, 9, 70])
 def test_refused_sequences_are_zero_in_what_is_allocated(tree, dev):
@@ -205,3 +285,30 @@ def test_huge_logits_pick_the_largest(tree, g, dtype, dev):
         head = (torch.arange(2 * g, device=dev) // g)[None, :, None].expand_as(pick)
         want = v[where // 64, head, where % 64]
         assert ((o.float() - want.float()).abs() <= 2.0 ** -9 * want.float().abs()).all()
+
+
+def test_tree_attn_outputs_and_workspaces_over_other_tensors(dev):
+    t = Tree(dev, BF16, 64, 16, 1, [20], [2], 2, junk=False)
+    c = _lib.Cache(1, t.k.shape[0], 1, 16, 64, 1, t.table.shape[1])
+    need = pbs.lib().pbs_tree_workspace_bytes(2, 2, c)
+    buf = torch.zeros(need + 8192, dtype=torch.uint8, device=dev)
+    q = torch.randn(1, 2, 2, 64, device=dev).to(BF16)
+    start, mask = i32([20], dev), i32([[[1], [3]]], dev)
+    want = pbs.tree_attn(q, t.k, t.v, t.table, start, mask)
+    ws, rest = buf[:need], buf[-(-need // 16) * 16:]
+    out = rest[:512].view(BF16).view(q.shape)
+    assert torch.equal(pbs.tree_attn(q, t.k, t.v, t.table, start, mask, out=out, ws=ws), want)
+    ints = ws[:8].view(torch.int32)
+    for kw in (dict(q=ws[:512].view(BF16).view(q.shape)), dict(out=ws[:512].view(BF16).view(q.shape)),
+               dict(k_pages=t.k, v_pages=buf[1024:1024 + 2 * t.v.numel()].view(BF16).view(t.v.shape)),
+               dict(start=ints[:1]), dict(count=ints[:1]), dict(mask=ints.view(1, 2, 1)),
+               dict(table=ints.view(1, 2))):
+        kw = dict(dict(q=q, k_pages=t.k, v_pages=t.v, table=t.table, start=start, mask=mask), **kw)
+        with pytest.raises((ValueError, pbs.PbsError)):
+            pbs.tree_attn(**kw, ws=ws)
+    over = out.view(torch.int32)
+    for kw in (dict(start=over.view(-1)[:1]), dict(mask=over.view(-1)[:2].view(1, 2, 1)),
+               dict(table=over.view(-1)[:2].view(1, 2))):
+        kw = dict(dict(table=t.table, start=start, mask=mask), **kw)
+        with pytest.raises((ValueError, pbs.PbsError)):
+            pbs.tree_attn(q, t.k, t.v, out=out, **kw)
