@@ -212,9 +212,10 @@ def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=No
     one launch (pbs_rope): bf16, fp16 or fp32, any strides with contiguous
     16-byte-aligned rows (slices of one projection). pos is int32 [b, n] or
     [n]; the first 2 * len(inv_freq) elements of each head turn. ``transpose``
-    turns back: the gradients of q and k from those of the results. Returns
-    (q', k'), or q' alone without k. q_out may be q itself and k_out k, and they
-    overlap nothing else."""
+    turns back: the gradients of q and k from those of the results, which
+    autograd takes where q or k requires one (then without q_out and k_out, and
+    inv_freq gets none). Returns (q', k'), or q' alone without k. q_out may be q
+    itself and k_out k, and they overlap nothing else."""
     _on(q, "q")
     dev, t, size = q.device, q.dtype, q.shape
     kind, order = _TYPES.get(t), _LAYOUTS.get(layout)
@@ -244,6 +245,13 @@ def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=No
         raise ValueError("inv_freq: 2 * len must be a multiple of 16 and at most d")
     each = isinstance(pos, torch.Tensor) and pos.dim() == 1
     _ints(pos, "pos", (n,) if each else (b, n), dev)
+    if (q.requires_grad or inv_freq.requires_grad or (k is not None and k.requires_grad)) and \
+            torch.is_grad_enabled():
+        if inv_freq.requires_grad:
+            raise ValueError("inv_freq has no gradient")
+        if not (q_out is None and k_out is None):
+            raise ValueError("q_out and k_out are not for inputs that require a gradient")
+        return _Rope.apply(q, k, pos, inv_freq, gain, layout, transpose)
     q_out, q_to = _rope_out(q, q_out, "q_out", hq, n, d)
     k_from = k_to = _NONE
     if k is not None:
@@ -256,6 +264,40 @@ def rope(q, k, pos, inv_freq, gain=1.0, layout="half", transpose=False, q_out=No
     return q_out if k is None else (q_out, k_out)
 
 
+class _Rope(torch.autograd.Function):
+    """rope under autograd. The map is linear, its gradient the transposed map,
+    which is a rope again (and so has a gradient itself)."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, inv_freq, gain, layout, transpose):
+        out = rope(q, k, pos, inv_freq, gain, layout, transpose)
+        ctx.save_for_backward(pos, inv_freq)
+        ctx.how = gain, layout, not transpose
+        ctx.set_materialize_grads(False)
+        return out
+
+    @staticmethod
+    def backward(ctx, *grads):
+        need = ctx.needs_input_grad[:2]
+        grads = [_readable(g) if n and g is not None else None
+                 for g, n in zip((*grads, None), need)]
+        there = [g for g in grads if g is not None]
+        if not there:
+            return (None,) * 7
+        back = rope(there[0], there[1] if len(there) > 1 else None, *ctx.saved_tensors, *ctx.how)
+        back = list(back) if len(there) > 1 else [back]
+        return (*(None if g is None else back.pop(0) for g in grads), *(None,) * 5)
+
+
+def _readable(g):
+    """A gradient as rope reads it: contiguous rows, 16-byte aligned."""
+    try:
+        _rows(g, "gradient")
+    except ValueError:
+        return g.clone(memory_format=torch.contiguous_format)
+    return g
+
+
 def _rope_out(x, y, name, h, n, d):
     """The tensor that takes x's result, and its rows."""
     if y is None:
@@ -264,6 +306,8 @@ def _rope_out(x, y, name, h, n, d):
     _on(y, name, x.device)
     if y.shape != x.shape or y.dtype is not x.dtype:
         raise ValueError(f"{name} must have the shape and type of its input")
+    if y.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} may not require a gradient")
     if y.data_ptr() != x.data_ptr() or y.stride() != x.stride():
         _apart(y, name, x)
     return y, _rows(y, name, True) if y.numel() else _NONE

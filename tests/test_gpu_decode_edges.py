@@ -4,12 +4,15 @@ types and lengths."""
 import math
 import random
 
+import numpy as np
 import pytest
 import torch
 
 import long_context_sparse_segment_b200 as pbs
 from long_context_sparse_segment_b200 import _lib
-from test_gpu_decode import Tree, bits, i32, ids
+from oracle import decode_oracle as dec
+from pbs_testutil import f64
+from test_gpu_decode import Tree, bits, i32, ids, rope_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -203,6 +206,99 @@ def test_rope_takes_just_the_outputs_that_are_apart(dev):
             assert torch.equal(base[rest.to(dev)], before[rest.to(dev)])
             taken += 1
     assert 100 < taken < 300
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+def test_rope_under_autograd(layout, dtype, dev):
+    """Gradients of q and k against the transposed map in fp64, against
+    differences, of one of the two alone, of expanded inputs, through expanded
+    and strided gradients, and of a gradient."""
+    b, hq, hkv, n, d, rot = 2, 6, 2, 11, 64, 48
+    f, pos = pbs.rope_freqs(rot)[0].to(dev), i32(np.arange(22).reshape(2, 11) * 991, dev)
+    make = lambda h: torch.randn(b, h, n, d, device=dev).to(dtype)
+    q, k, gq, gk = make(hq).requires_grad_(), make(hkv).requires_grad_(), make(hq), make(hkv)
+    how = dict(gain=1.25, layout=layout)
+    exact = lambda g: dec.rope(f64(g), pos.cpu().numpy(), f.cpu().numpy(), 1.25, layout, True)
+    near = lambda x, g: (np.abs(f64(x) - exact(g)) <= rope_bound(f64(g), exact(g), 1.25, dtype,
+                                                                 rot)).all()
+    y, z = pbs.rope(q, k, pos, f, **how)
+    plain = pbs.rope(q.detach(), k.detach(), pos, f, **how)
+    assert torch.equal(y, plain[0]) and torch.equal(z, plain[1]) and not plain[0].requires_grad
+    dq, dk = torch.autograd.grad((y, z), (q, k), (gq, gk), retain_graph=True)
+    assert near(dq, gq) and near(dk, gk) and dq.dtype == dtype
+    # one of the two alone; neither asked for
+    assert torch.equal(torch.autograd.grad(y, q, gq, retain_graph=True)[0], dq)
+    assert torch.equal(torch.autograd.grad(z, k, gk, retain_graph=True)[0], dk)
+    assert torch.autograd.grad(y, k, gq, allow_unused=True)[0] is None
+    assert torch.equal(torch.autograd.grad(pbs.rope(q, None, pos, f, **how), q, gq)[0], dq)
+    y, z = pbs.rope(q.detach(), k, pos, f, **how)
+    assert torch.equal(torch.autograd.grad(z, k, gk)[0], dk)
+    assert not y.requires_grad or torch.autograd.grad(y, k, gq, allow_unused=True)[0] is None
+    # gradients that repeat an element, or lie across
+    one = torch.ones((), dtype=dtype, device=dev)
+    dq1, = torch.autograd.grad(pbs.rope(q, None, pos, f, **how).sum(), q)
+    assert near(dq1, one.expand(b, hq, n, d))
+    across = torch.randn(b, hq, d, n, device=dev).to(dtype).transpose(2, 3)
+    assert near(torch.autograd.grad(pbs.rope(q, None, pos, f, **how), q, across)[0], across)
+    # heads and a batch that share an input: the sums of their gradients
+    s = make(hq)[:1, :1].requires_grad_()
+    ds, = torch.autograd.grad(pbs.rope(s.expand(b, hq, n, d), None, pos, f, **how), s, gq)
+    parts = f64(dq).sum((0, 1), keepdims=True)
+    # torch sums b hq rounded parts in fp32 and rounds once for the heads, once for the batch
+    size = np.abs(f64(dq)).sum((0, 1), keepdims=True)
+    assert (np.abs(f64(ds) - parts) <= 2.5 * torch.finfo(dtype).eps * size + b * hq * 2.0 ** -23
+            * size).all()
+    if dtype is FP32:  # along a direction: the map is linear
+        v = make(hq)
+        diff = f64(pbs.rope(q.detach() + v, None, pos, f, **how)) - f64(plain[0])
+        x, w = (diff * f64(gq)).sum(), (f64(v) * f64(dq)).sum()
+        size = sum((np.abs(f64(t)) * np.abs(f64(gq))).sum() for t in (q, v))
+        assert abs(x - w) <= 8 * 2.0 ** -23 * 1.25 * 2 * 6 * size
+    # the gradient of a gradient is the map itself
+    g = gq.clone().requires_grad_()
+    dq, = torch.autograd.grad(pbs.rope(q, None, pos, f, **how), q, g, create_graph=True)
+    assert torch.equal(torch.autograd.grad(dq, g, q.detach())[0], plain[0])
+
+
+def test_rope_under_autograd_refuses_and_captures(dev):
+    q = torch.randn(1, 4, 8, 64, device=dev, requires_grad=True)
+    f, pos = pbs.rope_freqs(64)[0].to(dev), torch.arange(8, dtype=torch.int32, device=dev)
+    for kw in (dict(q_out=torch.empty_like(q)), dict(inv_freq=f.clone().requires_grad_()),
+               dict(k=q.detach(), k_out=torch.empty_like(q))):
+        with pytest.raises(ValueError):
+            pbs.rope(**dict(dict(q=q, k=None, pos=pos, inv_freq=f), **kw))
+    with torch.no_grad():
+        y = torch.empty_like(q)
+        assert pbs.rope(q, None, pos, f, q_out=y) is y and not y.requires_grad
+    assert not pbs.rope(q.detach(), None, pos, f).requires_grad
+    with pytest.raises(ValueError):
+        pbs.rope(q.detach(), None, pos, f, q_out=torch.empty_like(q).requires_grad_())
+    # positions that change before the backward pass are noticed
+    z = pbs.rope(q, None, pos, f)
+    pos += 1
+    with pytest.raises(RuntimeError):
+        z.sum().backward()
+    del z
+    # forward and backward as one graph
+    x, g = torch.randn_like(q), torch.randn_like(q)
+
+    def step():
+        leaf = x.detach().requires_grad_()
+        y = pbs.rope(leaf, None, pos, f)
+        return y.detach(), torch.autograd.grad(y, leaf, g)[0]
+
+    side, graph = torch.cuda.Stream(dev), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = step()
+    x.copy_(torch.randn_like(x)), g.copy_(torch.randn_like(g)), pos.add_(100)
+    graph.replay()
+    want = step()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 # ------------------------------------------------------------------- attention
