@@ -14,9 +14,12 @@
 // Angles. t f in fp32 is off by up to t f 2^-24 radians (0.008 at 131072),
 // more than a bf16 result's rounding, and fp64 sine and cosine are slow. So
 // f is turned into a 64-bit fixed-point fraction of a turn; t times it in
-// integers, modulo 2^64, is the angle modulo one turn without rounding, and
-// its upper 32 bits go through sincospif. What is left is f's own rounding
-// (2^-53 relative, times t) and fp32's 2^-24 of half a turn.
+// integers, modulo 2^64, is the angle modulo one turn without rounding. The
+// nearest quarter turn comes off in integers too; what remains is at most an
+// eighth of a turn, is cut to 2^-34 turns, rounds to fp32 within 2^-24 of itself and
+// goes through sincospif. So an angle is off by pi (2^-27 + 2^-33) radians at most
+// (rounded at once, with a half turn's bits: four times as much), besides f's own
+// rounding (2^-53 relative, times t).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -125,10 +128,17 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       double f = __ldg(a.inv_freq + u * V + e) * 0.15915494309189535;  // turns per position
       f -= floor(f);
       const uint64_t angle = t * (uint64_t)(f * 18446744073709551616.0);
-      // upper 32 bits as a signed fraction: half turns in [-1, 1)
-      sincospif((float)(int32_t)(angle >> 32) * 4.656612873077393e-10f, &s[e], &c[e]);
-      c[e] *= a.gain;
-      s[e] *= a.transpose ? -a.gain : a.gain;
+      // an eighth of a turn further: whole quarters in the upper two bits, and the
+      // rest, less that eighth, in [-1/8, 1/8) turns, its upper 32 bits in 2^-34
+      const uint32_t high = (uint32_t)(angle >> 32) + (1u << 29);
+      const uint32_t quarter = high >> 30;
+      const uint32_t rest = (high << 2 | (uint32_t)angle >> 30) - (1u << 31);
+      float sn, cs;
+      sincospif((float)(int32_t)rest * 0x1p-33f, &sn, &cs);  // half turns
+      const uint32_t x = __float_as_uint(quarter & 1 ? sn : cs);
+      const uint32_t y = __float_as_uint(quarter & 1 ? cs : sn);
+      c[e] = __uint_as_float(x ^ ((quarter + 1) & 2) << 30) * a.gain;
+      s[e] = __uint_as_float(y ^ (quarter & 2) << 30) * (a.transpose ? -a.gain : a.gain);
     }
   }
   const int h0 = blockIdx.y * a.heads_per, h1 = min(h0 + a.heads_per, a.heads);

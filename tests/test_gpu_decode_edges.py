@@ -208,6 +208,37 @@ def test_rope_takes_just_the_outputs_that_are_apart(dev):
     assert 100 < taken < 300
 
 
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_angles_of_rope_in_fp32(transpose, layout, dev):
+    """The cosine and sine of angles all over the turn, close to and on the
+    quarters among them: an eighth of a turn, cut to 2^-34 turns, rounds to fp32
+    within pi 2^-27, and sincospif is within a step of 2^-24. The oracle's angle comes from the same
+    fp64 frequency, reduced in whole numbers."""
+    n = 1 << 18
+    x = torch.zeros(1, 1, n, 16, device=dev)
+    at = (0, 8) if layout == "half" else (0, 1)
+    x[..., at[0]] = 1
+    pos = torch.arange(n, dtype=torch.int32)
+    pos[n // 2:] = torch.randint(-2 ** 31, 2 ** 31 - 1, (n // 2,),
+                                 generator=torch.Generator().manual_seed(1)).int()
+    for turn in (0.11637718, 1 / 8 + 2.0 ** -30, 1 / 4, 1 / 4 - 2.0 ** -33, 0.5, 3 / 16):
+        f = torch.zeros(8, dtype=torch.float64)
+        f[0] = turn * 2 * math.pi
+        y = f64(pbs.rope(x, None, pos.to(dev), f.to(dev), 1.0, layout, transpose))[0, 0]
+        # turns of the frequency as the call gets it, a whole number of 2^-64 as it keeps them
+        whole = int(math.floor((float(f[0]) * 0.15915494309189535 % 1.0) * 2.0 ** 64))
+        rest = [p * whole % 2 ** 64 for p in pos.tolist()]
+        part = np.array([(z + 2 ** 61) % 2 ** 62 - 2 ** 61 for z in rest], dtype=np.float64)
+        a = part * (2 * math.pi / 2.0 ** 64)
+        cs, sn = np.cos(a), np.sin(a)
+        quarter = np.array([(z + 2 ** 61) // 2 ** 62 % 4 for z in rest])
+        cos = np.choose(quarter, [cs, -sn, -cs, sn])
+        sin = np.choose(quarter, [sn, cs, -sn, -cs]) * (-1 if transpose else 1)
+        tol = math.pi * (2.0 ** -27 + 2.0 ** -33) + 2.0 ** -24
+        assert np.abs(y[:, at[0]] - cos).max() <= tol and np.abs(y[:, at[1]] - sin).max() <= tol
+
+
 @pytest.mark.parametrize("dtype", [FP32, BF16])
 @pytest.mark.parametrize("layout", ["half", "pairs"])
 def test_rope_under_autograd(layout, dtype, dev):
