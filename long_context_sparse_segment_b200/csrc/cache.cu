@@ -475,14 +475,16 @@ __global__ void __launch_bounds__(kAcceptThreads)
 
 // The lengths behind an acceptance whose `start` or `count` is `lens` itself: the
 // rows' kernel reads those in every block of a sequence until its end, so the
-// lengths are written behind it, where the path is good (one block a sequence, 2 us).
+// lengths are written behind it, where the path is good (one block a sequence, 2 us);
+// and behind one of no rows at all.
 __global__ void __launch_bounds__(kAcceptThreads)
     accept_lens_kernel(const int32_t *__restrict__ table, const int32_t *start,
                        const int32_t *__restrict__ path, const int32_t *count, int32_t *lens,
-                       int tree, pbs_cache c) {
+                       int tree, pbs_cache c, int *err) {
   const int s = blockIdx.x;
   const int n = count ? min(count[s], tree) : tree, st = start[s];
   bool bad = st < 0;
+  if (bad && threadIdx.x == 0) report(err, PBS_ERR_DEVICE_ASSERT);
   for (int i = threadIdx.x; i < n; i += kAcceptThreads) {
     int64_t from, to;
     bad |= !accept_row(table + (size_t)s * c.width, path + (size_t)s * tree, i, st, c, c.d / 8,
@@ -638,7 +640,16 @@ pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,
                             int32_t *lens, int tree, pbs_cache c, pbs_stream_t st) {
   if (!cache_ok(c) || tree < 0) return PBS_ERR_INVALID_ARG;
   if (c.seqs > 65535) return PBS_ERR_UNSUPPORTED;
-  if (c.seqs == 0 || tree == 0) return PBS_OK;
+  if (c.seqs == 0) return PBS_OK;
+  if (tree == 0) {  // nothing moves, the lengths are the starts
+    if (!lens || lens == start) return PBS_OK;
+    const int64_t each = 4ll * c.seqs;
+    if (!ints_ok(start) || !ints_ok(lens) || bytes_meet(lens, each, start, each))
+      return PBS_ERR_INVALID_ARG;
+    accept_lens_kernel<<<c.seqs, kAcceptThreads, 0, (cudaStream_t)st>>>(
+        nullptr, start, nullptr, nullptr, lens, 0, c, error_word());
+    return done();
+  }
   // one pool for both would be moved twice at once
   if (!pool_ok(k_pages) || !pool_ok(v_pages) || k_pages == v_pages || !ints_ok(table) ||
       !ints_ok(start) || !ints_ok(path) || (count && !ints_ok(count)) || (lens && !ints_ok(lens)) ||
@@ -660,7 +671,8 @@ pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,
       c, col_blocks, error_word());
   if (behind)
     accept_lens_kernel<<<c.seqs, kAcceptThreads, 0, (cudaStream_t)st>>>(table, start, path, count,
-                                                                       lens, tree, c);
+                                                                       lens, tree, c,
+                                                                       error_word());
   return done();
 }
 

@@ -79,6 +79,24 @@ def test_accept_refuses_lengths_inside_other_inputs(dev):
             pbs.cache_accept(k, v, table, **dict(dict(path=path), **kw))
 
 
+def test_accept_of_an_empty_path_sets_the_lengths(dev):
+    k, v = (ids((4, 1, 16, 64), dev, seed=s) for s in (1, 2))
+    table, none = i32([[0, 1], [2, 3], [0, 1]], dev), torch.zeros(3, 0, dtype=torch.int32, device=dev)
+    lens = i32([9, 9, 9], dev)
+    pbs.cache_accept(k, v, table, i32([3, 4, -1], dev), none, lens=lens)
+    assert pbs.device_status() == _lib.ERR_DEVICE_ASSERT  # the negative one
+    assert lens.tolist() == [3, 4, 9]
+    pbs.cache_accept(k, v, table, lens, none, lens=lens)
+    pbs.cache_accept(k, v, table, i32([1, 2, 3], dev), none)
+    pbs.cache_accept(k, v, table[:0], lens[:0], none[:0], lens=lens[:0])
+    assert lens.tolist() == [3, 4, 9]
+    with pytest.raises(pbs.PbsError):
+        pbs.cache_accept(k, v, table[:2], lens[:2], none[:2], lens=lens[1:])
+    # no row of a longer path
+    pbs.cache_accept(k, v, table, i32([1, 2, 3], dev), i32([[0]] * 3, dev), i32([0, -2, 0], dev), lens)
+    assert lens.tolist() == [1, 2, 3]
+
+
 @pytest.mark.parametrize("whole", [False, True])
 def test_nothing_is_written_into_shared_pages_behind_a_failed_reserve(whole, dev):
     """A fork cut back to the middle of a shared page, a full pool, and the calls
