@@ -506,6 +506,14 @@ def tree_mask(parents):
     return mask, depth
 
 
+def _tree_bytes(dev, hq, tree, c):
+    """The workspace of tree_attn on device ``dev``: it grows with its SMs."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return lib().pbs_tree_workspace_bytes(hq, tree, c)
+    return lib().pbs_tree_workspace_bytes(hq, tree, c)
+
+
 def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.0, lse=False,
               out=None, ws=None):
     """Attention of q [seqs, hq, tree, d] (bf16 or fp16, strided rows) over one
@@ -549,7 +557,7 @@ def tree_attn(q, k_pages, v_pages, table, start, mask=None, count=None, scale=0.
         l = make((seqs, hq, tree), dtype=torch.float32)
     if not (seqs and tree):
         return (out, l) if lse else out
-    need = lib().pbs_tree_workspace_bytes(hq, tree, c)
+    need = _tree_bytes(dev, hq, tree, c)
     if ws is None:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     else:

@@ -107,3 +107,31 @@ def test_written_rows_that_meet_other_memory_are_refused():
         p[i] = FAKE  # the workspace's place
         assert call_tree(cache(), ptrs=p, q=rows(p=1 << 40)) == _lib.ERR_INVALID_ARG, name
     assert call_tree(cache(), ptrs=apart, q=rows(p=1 << 31)) == _lib.ERR_INVALID_ARG  # q is out
+
+
+def test_workspaces_are_sized_on_the_tensors_device(monkeypatch):
+    """Two devices of different SM counts, faked: the size is asked for with the
+    tensors' device current, and the current one is put back."""
+    from long_context_sparse_segment_b200 import decode
+    now = [0]
+
+    class Device:
+        def __init__(self, dev):
+            self.to = dev.index
+
+        def __enter__(self):
+            self.back, now[0] = now[0], self.to
+
+        def __exit__(self, *_):
+            now[0] = self.back
+
+    class Lib:
+        @staticmethod
+        def pbs_tree_workspace_bytes(hq, tree, c):
+            return (100, 132)[now[0]] * hq * tree
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(decode, "lib", Lib)
+    sizes = [decode._tree_bytes(torch.device("cuda", i), 2, 3, cache()) for i in (0, 1, 0)]
+    assert sizes == [600, 792, 600] and now == [0]
