@@ -509,7 +509,7 @@ int pieces(const pbs_cache &c) { return (int)ceil_div(page_words(c), kPiece); }
 
 unsigned copy_grid(const pbs_cache &c, int64_t pairs) {
   // eight CTAs of 256 threads fit an SM
-  const int64_t w = 2LL * c.layers * pieces(c) * pairs, most = 148LL * 8 * 4;
+  const int64_t w = 2LL * c.layers * pieces(c) * pairs, most = 8LL * 4 * sm_count_cached();
   return (unsigned)(w < most ? w : most);
 }
 
@@ -559,7 +559,7 @@ pbs_status pbs_cache_append(pbs_rows k, pbs_rows v, int n, void *k_pages, void *
       (c.refs && !ints_ok(c.refs)))
     return PBS_ERR_INVALID_ARG;
   const int64_t total = (int64_t)c.layers * c.seqs * c.hkv * n * (c.d / 8);
-  const int64_t blocks = ceil_div(total, 256), most = 148 * 32;
+  const int64_t blocks = ceil_div(total, 256), most = 32 * sm_count_cached();
   append_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, (cudaStream_t)st>>>(
       k, v, n, (uint4 *)k_pages, (uint4 *)v_pages, table, start, count, c, total, error_word());
   return done();

@@ -271,7 +271,7 @@ extern "C" pbs_status pbs_rope(pbs_rows q, pbs_rows q_out, int hq, pbs_rows k, p
   // few tokens: the heads are split over blocks until there are sixteen blocks
   // an SM, and the angles computed again in each (12252 tokens of 15 fp32 heads:
   // 33.7 us, with eight blocks an SM 35.8)
-  int64_t split = ceil_div(148 * 16, bx);
+  int64_t split = ceil_div(16 * sm_count_cached(), bx);
   if (split > a.heads) split = a.heads;
   a.heads_per = (int)ceil_div(a.heads, split);
   if (ceil_div(a.heads, a.heads_per) > 65535) return PBS_ERR_UNSUPPORTED;

@@ -109,6 +109,13 @@ def test_written_rows_that_meet_other_memory_are_refused():
     assert call_tree(cache(), ptrs=apart, q=rows(p=1 << 31)) == _lib.ERR_INVALID_ARG  # q is out
 
 
+def test_grids_follow_the_device():
+    """No launch of the decoding operators takes the SMs for a constant."""
+    csrc = pathlib.Path(_lib.LIB_PATH).parent / "csrc"
+    for f in ("rope.cu", "cache.cu", "tree.cu", "tree.cuh", "tree_tc.cu", "decode.h"):
+        assert not re.search(r"\b148\b", re.sub(r"//[^\n]*", "", (csrc / f).read_text())), f
+
+
 def test_workspaces_are_sized_on_the_tensors_device(monkeypatch):
     """Two devices of different SM counts, faked: the size is asked for with the
     tensors' device current, and the current one is put back."""
