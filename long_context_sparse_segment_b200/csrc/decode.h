@@ -32,12 +32,19 @@ struct RowSet {
   pbs_rows r;
   int64_t batch, heads, n;
   int d, elem;
-  // elements from the first one to behind the last
-  int64_t span() const {
-    return r.batch * (batch - 1) + r.head * (heads - 1) + r.row * (n - 1) + d;
-  }
-  bool plain() const { return r.batch >= 0 && r.head >= 0 && r.row >= 0; }
+  // the bytes from the lowest element, and how many up to behind the highest
+  const uint8_t *low() const { return (const uint8_t *)r.p + elem * reach(-1); }
+  int64_t bytes() const { return elem * (reach(1) - reach(-1) + d); }
+  bool plain() const { return reach(-1) == 0; }  // no stride runs backwards
   bool empty() const { return batch <= 0 || heads <= 0 || n <= 0 || d <= 0; }
+
+ private:
+  int64_t reach(int sign) const {  // elements from p to the last row that way
+    auto part = [&](int64_t stride, int64_t size) {
+      return stride * sign > 0 ? stride * (size - 1) : 0;
+    };
+    return part(r.batch, batch) + part(r.head, heads) + part(r.row, n);
+  }
 };
 
 // Whether two sets of rows share memory: element by element where their strides

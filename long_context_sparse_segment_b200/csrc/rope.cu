@@ -205,15 +205,14 @@ bool dims_meet(const MeetDim *dims, int k, int64_t off, int d) {
 
 bool rows_meet(const RowSet &x, const void *p, int64_t bytes) {
   if (x.empty()) return false;
-  return !x.plain() || bytes_meet(x.r.p, x.span() * x.elem, p, bytes);
+  return bytes_meet(x.low(), x.bytes(), p, bytes);
 }
 
 bool rows_meet(const RowSet &x, const RowSet &y) {
   if (x.empty() || y.empty()) return false;
-  if (!x.plain() || !y.plain()) return true;
-  if (!bytes_meet(x.r.p, x.span() * x.elem, y.r.p, y.span() * y.elem)) return false;
+  if (!bytes_meet(x.low(), x.bytes(), y.low(), y.bytes())) return false;
   const int64_t bytes = (intptr_t)y.r.p - (intptr_t)x.r.p;
-  if (x.elem != y.elem || x.d != y.d || bytes % x.elem) return true;
+  if (!x.plain() || !y.plain() || x.elem != y.elem || x.d != y.d || bytes % x.elem) return true;
   const int64_t s[2][3] = {{x.r.batch, x.r.head, x.r.row}, {y.r.batch, y.r.head, y.r.row}};
   const int64_t n[2][3] = {{x.batch, x.heads, x.n}, {y.batch, y.heads, y.n}};
   MeetDim dims[3];
@@ -253,7 +252,9 @@ extern "C" pbs_status pbs_rope(pbs_rows q, pbs_rows q_out, int hq, pbs_rows k, p
                           {k, batch, hkv, n, d, elem},
                           {q_out, batch, hq, n, d, elem},
                           {k_out, batch, hkv, n, d, elem}};
-  const int64_t pos_bytes = 4 * ((pos_batch < 0 ? -pos_batch : pos_batch) * (batch - 1) + n);
+  const int64_t pos_reach = pos_batch * (batch - 1);
+  const int32_t *pos_low = pos + (pos_reach < 0 ? pos_reach : 0);
+  const int64_t pos_bytes = 4 * ((pos_reach < 0 ? -pos_reach : pos_reach) + n);
   for (int o = 2; o < 4; ++o) {
     for (int i = 0; i < o; ++i) {
       const pbs_rows &x = sets[i].r, &y = sets[o].r;
@@ -261,7 +262,7 @@ extern "C" pbs_status pbs_rope(pbs_rows q, pbs_rows q_out, int hq, pbs_rows k, p
                        (sets[i].heads == 1 || x.head == y.head) && (n == 1 || x.row == y.row);
       if (!own && rows_meet(sets[i], sets[o])) return PBS_ERR_INVALID_ARG;
     }
-    if (rows_meet(sets[o], pos, pos_bytes) || rows_meet(sets[o], inv_freq, 4ll * rot))
+    if (rows_meet(sets[o], pos_low, pos_bytes) || rows_meet(sets[o], inv_freq, 4ll * rot))
       return PBS_ERR_INVALID_ARG;
   }
   RopeArgs a{q, q_out, k, k_out, pos, inv_freq, pos_batch, (int64_t)batch * n, gain};

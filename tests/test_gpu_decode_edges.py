@@ -226,6 +226,28 @@ def test_rope_takes_just_the_outputs_that_are_apart(dev):
     assert 100 < taken < 300
 
 
+def test_rope_rows_that_run_backwards(dev):
+    """Rows from the last to the first through the C ABI: into their own places,
+    into places behind them, and over one another (refused)."""
+    n, d = 6, 64
+    f, pos = pbs.rope_freqs(d)[0].to(dev), torch.arange(n, dtype=torch.int32, device=dev)
+    buf = torch.randn(3 * n, d, device=dev).to(BF16)
+    before = buf.clone()
+    want = pbs.rope(before[:n].flip(0)[None, None], None, pos, f)[0, 0].flip(0)
+
+    def call(src, dst):  # from row src and to row dst down
+        rows = [_lib.Rows(buf[x].data_ptr(), 0, 0, 0, -d) for x in (src, dst)]
+        none = _lib.Rows(None, 0, 0, 0, 0)
+        return pbs.lib().pbs_rope(*rows, 1, none, none, 0, pos.data_ptr(), 0, f.data_ptr(), 1.0, 1, n,
+                                  d, d, 0, 0, _lib.BF16, torch.cuda.current_stream(dev).cuda_stream)
+
+    assert call(n - 1, n + 1) == _lib.ERR_INVALID_ARG and call(n + 1, n - 1) == _lib.ERR_INVALID_ARG
+    assert torch.equal(buf, before)
+    assert call(n - 1, 2 * n - 1) == 0 and torch.equal(buf[n:2 * n], want)
+    assert torch.equal(buf[:n], before[:n]) and torch.equal(buf[2 * n:], before[2 * n:])
+    assert call(n - 1, n - 1) == 0 and torch.equal(buf[:n], want)
+
+
 @pytest.mark.parametrize("layout", ["half", "pairs"])
 @pytest.mark.parametrize("transpose", [False, True])
 def test_angles_of_rope_in_fp32(transpose, layout, dev):
