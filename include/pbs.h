@@ -520,8 +520,8 @@ pbs_status pbs_cache_reserve(int32_t *table, int32_t *refs, const int32_t *lens,
 /*
  * pbs_cache_append - rows i < count[s] (all n when count is NULL) of k, v
  * [layers, seqs, hkv, n, d] written at tokens start[s] + i. The pages must
- * be reserved, k and v lie outside the pools, the pools apart. No other row of
- * the pools is touched. Rows without a page, or with c.refs on a page that
+ * be reserved, k and v (by the memory that they span) lie outside the pools, and
+ * the pools apart: refused. No other row of the pools is touched. Rows without a page, or with c.refs on a page that
  * several sequences hold, are reported and skipped.
  */
 pbs_status pbs_cache_append(pbs_rows k, pbs_rows v, int n, void *k_pages, void *v_pages,
@@ -572,7 +572,8 @@ pbs_status pbs_cache_compact(void *k_pages, void *v_pages, int32_t *table, int32
  * [seqs, n] ascends strictly from 0 on, so a draft only moves down; a
  * sequence whose path does not, or names a token that no page holds, is
  * reported and left alone.
- * The pages from token start[s] on must be the sequence's own (reserved); with
+ * The pools lie apart. The pages from token start[s] on must be the sequence's own
+ * (reserved); with
  * c.refs a sequence whose accepted tokens come to lie in a page that several
  * hold is reported and left alone too.
  * lens (may be NULL): lens[s] = start[s] + count[s] where the path is good. It

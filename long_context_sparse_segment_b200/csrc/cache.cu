@@ -504,6 +504,9 @@ bool ints_ok(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
 bool pool_ok(const void *p) { return p && ((uintptr_t)p & 15u) == 0; }
 pbs_status done() { return cudaGetLastError() == cudaSuccess ? PBS_OK : PBS_ERR_CUDA; }
 
+int64_t pool_bytes(const pbs_cache &c) {
+  return 2ll * c.layers * c.pages * c.hkv * c.page * c.d;
+}
 int64_t page_words(const pbs_cache &c) { return (int64_t)c.hkv * c.page * c.d / 8; }
 int pieces(const pbs_cache &c) { return (int)ceil_div(page_words(c), kPiece); }
 
@@ -558,6 +561,20 @@ pbs_status pbs_cache_append(pbs_rows k, pbs_rows v, int n, void *k_pages, void *
       k_pages == v_pages || !ints_ok(table) || !ints_ok(start) || (count && !ints_ok(count)) ||
       (c.refs && !ints_ok(c.refs)))
     return PBS_ERR_INVALID_ARG;
+  // the pools, apart from one another, hold neither the rows nor what says where
+  // they go
+  const int64_t pool = pool_bytes(c), each = 4ll * c.seqs;
+  bool meet = bytes_meet(k_pages, pool, v_pages, pool);
+  for (const void *to : {(const void *)k_pages, (const void *)v_pages}) {
+    for (const pbs_rows &x : {k, v}) {
+      const RowSet rows{x, c.seqs, c.hkv, n, c.d, 2};
+      const int64_t up = 2 * x.layer * (c.layers - 1);  // bytes from the first layer to the last
+      meet |= bytes_meet(rows.low() + (up < 0 ? up : 0), rows.bytes() + (up < 0 ? -up : up), to, pool);
+    }
+    meet |= bytes_meet(to, pool, table, each * c.width) || bytes_meet(to, pool, start, each) ||
+            bytes_meet(to, pool, count, each) || bytes_meet(to, pool, c.refs, 4ll * c.pages);
+  }
+  if (meet) return PBS_ERR_INVALID_ARG;
   const int64_t total = (int64_t)c.layers * c.seqs * c.hkv * n * (c.d / 8);
   const int64_t blocks = ceil_div(total, 256), most = 32 * sm_count_cached();
   append_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, (cudaStream_t)st>>>(
@@ -656,8 +673,9 @@ pbs_status pbs_cache_accept(void *k_pages, void *v_pages, const int32_t *table,
       (c.refs && !ints_ok(c.refs)))
     return PBS_ERR_INVALID_ARG;
   // lens may be start or count, but otherwise nothing that other sequences read
-  const int64_t each = 4ll * c.seqs;
-  if ((lens != start && bytes_meet(lens, each, start, each)) ||
+  const int64_t each = 4ll * c.seqs, pool = pool_bytes(c);
+  if (bytes_meet(k_pages, pool, v_pages, pool) ||
+      (lens != start && bytes_meet(lens, each, start, each)) ||
       (lens != count && bytes_meet(lens, each, count, each)) ||
       bytes_meet(lens, each, path, each * tree) || bytes_meet(lens, each, table, each * c.width) ||
       bytes_meet(lens, each, c.refs, 4ll * c.pages))

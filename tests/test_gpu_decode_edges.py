@@ -97,6 +97,36 @@ def test_accept_of_an_empty_path_sets_the_lengths(dev):
     assert lens.tolist() == [1, 2, 3]
 
 
+@pytest.mark.parametrize("lead", [(), (2,)])
+def test_append_refuses_rows_inside_the_pools(lead, dev):
+    """k or v cut out of a pool, pools that share pages, and tables there; a
+    neighbour of the pools in one allocation is taken."""
+    size = (*lead, 4, 1, 16, 64)
+    n = 2 * 64 * 16 * 4 // 2 * (lead[0] if lead else 1)
+    big = ids((4 * n,), dev, seed=1)
+    k, v, new = (big[i * n:(i + 1) * n].view(size) for i in range(3))
+    rows = new.view(*lead, 2, 2, 16, 64)[..., :1, :3, :]  # [.., seqs, 1, 3, 64]
+    table, start = i32([[0], [1]], dev), i32([2, 5], dev)
+    inside = k.view(*lead, 2, 2, 16, 64)[..., :1, :3, :]
+    ints = v.view(torch.int32).view(-1)
+    before = bits(big).clone()
+    for kw in (dict(k=inside), dict(v=inside), dict(v_pages=k),
+               dict(v_pages=big[n // 4:n // 4 + n].view(size)), dict(table=ints[:2].view(2, 1)),
+               dict(start=ints[2:4]), dict(count=ints[2:4])):
+        with pytest.raises(pbs.PbsError):
+            pbs.cache_append(**dict(dict(k=rows, v=rows, k_pages=k, v_pages=v, table=table,
+                                         start=start), **kw))
+    with pytest.raises(pbs.PbsError):
+        pbs.cache_accept(k, big[n // 4:n // 4 + n].view(size), table, start, i32([[0], [0]], dev))
+    assert torch.equal(bits(big), before)
+    pbs.cache_append(rows, rows, k, v, table, start)
+    for s in range(2):
+        at = int(start[s])
+        for pool in (k, v):
+            assert torch.equal(bits(pool[..., s, :, at:at + 3, :]), bits(rows[..., s, :, :, :]))
+    assert torch.equal(bits(big)[2 * n:], before[2 * n:])
+
+
 @pytest.mark.parametrize("whole", [False, True])
 def test_nothing_is_written_into_shared_pages_behind_a_failed_reserve(whole, dev):
     """A fork cut back to the middle of a shared page, a full pool, and the calls
