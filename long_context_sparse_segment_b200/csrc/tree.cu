@@ -18,8 +18,8 @@
 // busy for 1,450 cycles, two warps a scheduler, while its 32 KB (d = 128) take
 // 1,450 to arrive at the copy rate: the tensor core of tcgen05 would have 4 to
 // 16 of its 128 rows to do. Measured: a new token of each of 48 sequences of
-// 100 to 32768 tokens (3.29 GB of K and V) 493-509 us, 6.5-6.7 TB/s (the copy
-// rate is 6.56); one sequence of 8192 tokens 17 us, of which the bytes are 5
+// 100 to 32768 tokens (3.29 GB of K and V) 490-502 us, 6.6-6.7 TB/s (the copy
+// rate is 6.56); one sequence of 8192 tokens 16 us, of which the bytes are 5
 // and the rest launches, the run's start and the combining kernel.
 #include <stdlib.h>
 #include <string.h>
@@ -472,8 +472,9 @@ int row_tile(int hq, int tree, const pbs_cache &c) {
 // SM. Two CTAs hide the 2 to 4 us that an item's beginning and end cost, and
 // have two warps to issue the copies, where 16-token pages of d = 64 keep one
 // busy; their twice as many runs leave more parts to join, and a long item reads
-// a little slower. Us a call (4 rows, 8 KV heads, captured; one block a head
-// in the joining kernel, whose later form takes 37 off 2000 x 50, 8 off 512 x 200):
+// a little slower. Us a call (4 rows, 8 KV heads, captured, taken with one block a
+// head in the joining kernel; its later form takes 40 off 2000 x 50 and 9 off 512 x
+// 200, the later scan for a run's place 10 more off the former):
 //   d, page   sequences x tokens       8 warps   2 x 4
 //   128, 64    2000 x 50                  395.8   227.3
 //   128, 64    512 x 200                  148.2   108.0

@@ -122,8 +122,9 @@ __device__ __forceinline__ int cdiv(int x, int y) { return (x + y - 1) / y; }
 // counted in front of an item's own, and a run that begins an item gets fewer
 // tiles. Measured with clocks in the kernels: 7 us of 1.9 us tiles (256 rows),
 // 5 of 1.6 (128 rows), 1.5 of 0.7 (16 rows, 64 keys). Without it 7 drafts over
-// 128K tokens take 110 instead of 106 us, 64 drafts of 64 sequences of 1000
-// tokens 166 instead of 160; twice as much changes nothing more.
+// 128K tokens take 94.4 instead of 92.4 us, one sequence of 8K 17.1 instead of 15.9,
+// 64 drafts of 64 sequences of 1000 tokens 160-170 instead of 155-161; twice as
+// much: 92.4, 15.4 and 151.
 template <int ROWS>
 constexpr int kExtra = ROWS == 16 ? 2 : 3;
 

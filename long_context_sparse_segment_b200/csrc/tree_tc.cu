@@ -19,12 +19,14 @@
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (D each).
 //
 // What bounds it. 256 rows: a tile takes 3,490 cycles, in which the tensor core
-// has 2,048 of products (47 % busy) and the exponentials 2,048 (XU 53 %): a
-// stream's softmax and products follow one another, and the two streams overlap
-// as far as the one in-order tensor core lets them. Up to 128 rows: reading the
-// cache. Measured: 64 drafts of 8 sequences of 8K to 32K tokens 147 us a call
-// (170 under the power limit), 755 TFLOP/s, of which 128 us are this kernel;
-// 7 drafts over 131072 tokens 102 us, of which 88 are this kernel (6.1 TB/s).
+// has 2,048 of products (59 %) and the exponentials 2,048: a stream's softmax and
+// products follow one another, and the two streams overlap as far as the one
+// in-order tensor core lets them. (Over a whole call of 8 sequences of 16K tokens,
+// with its start, items' ends and parts, the profiler has the tensor core 46 % and
+// the XU 53 % busy.) Up to 128 rows: reading the cache. Measured on the device: 64
+// drafts of 8 sequences of 8K to 32K tokens 139 us (157 under the power limit), 800
+// TFLOP/s of drafts, of which 128 us are this kernel; 7 drafts over 131072 tokens
+// 92.7 us, of which 88 are this kernel (6.1 TB/s).
 #include "internal.h"
 #include "tree_tc.h"
 
