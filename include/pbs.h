@@ -483,10 +483,10 @@ typedef struct {
   int d;    /* a multiple of 8; 64 or 128 for pbs_tree_attn */
   int seqs, width;
   /* NULL, or the reference counts for pbs_cache_append and pbs_cache_accept
-   * (the calls that take refs of their own do not read it): they then write
-   * only into pages that one sequence holds alone, refs == 1, and report and
-   * leave the others. So a pbs_cache_reserve that found too few free pages
-   * cannot end in writes to another sequence's tokens. */
+   * (the calls that take refs of their own do not read it): they then report
+   * and leave what they would write into a page that several sequences hold.
+   * So a pbs_cache_reserve that found too few free pages cannot end in writes
+   * to another sequence's tokens. */
   const int32_t *refs;
 } pbs_cache;
 

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 // ------------------------------------------------------------ append, accept
 // The word offset of token t of sequence s in one layer's pool (head 0, first
 // word), or -1 for a token that no page holds; `write`: or, with c.refs, one
-// whose page is not the sequence's alone.
+// whose page several sequences hold.
 __device__ __forceinline__ int64_t token_word(const int32_t *row, int64_t t, const pbs_cache &c,
                                               int words, bool write) {
   if (t < 0 || t > 0x7fffffff) return -1;
@@ -368,7 +368,7 @@ __device__ __forceinline__ int64_t token_word(const int32_t *row, int64_t t, con
   if (j >= (unsigned)c.width) return -1;
   const int page = row[j];
   if (page < 0 || page >= c.pages) return -1;
-  if (write && c.refs && c.refs[page] != 1) return -1;
+  if (write && c.refs && c.refs[page] > 1) return -1;
   return ((int64_t)page * c.hkv * c.page + ((unsigned)t - j * c.page)) * words;
 }
 

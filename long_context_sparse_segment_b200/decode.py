@@ -390,7 +390,7 @@ def cache_reserve(table, refs, lens, want, page):
 
 
 def _owned(c, refs, device):
-    """``refs`` put into c: writes only into pages that one sequence holds alone."""
+    """``refs`` put into c: no writes into pages that several sequences hold."""
     if refs is not None:
         _ints(refs, "refs", (c.pages,), device)
         c.refs = refs.data_ptr()

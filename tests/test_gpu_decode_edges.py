@@ -97,6 +97,24 @@ def test_accept_of_an_empty_path_sets_the_lengths(dev):
     assert lens.tolist() == [1, 2, 3]
 
 
+def test_tables_of_ones_own_need_no_reference_counts(dev):
+    """A PagedCache whose table the caller fills, its counts left at 0."""
+    c = pbs.PagedCache(2, 32, 4, 1, 64, 16, 1, BF16, dev)
+    c.table.copy_(i32([[3, 1], [0, 2]], dev))
+    new = ids((2, 1, 5, 64), dev, seed=1)
+    c.append(0, new, new, start=i32([13, 2], dev))
+    assert pbs.device_status() == 0
+    for pool in (c.k, c.v):
+        got = bits(pool)[0]
+        assert torch.equal(got[3, :, 13:], bits(new)[0, :, :3])
+        assert torch.equal(got[1, :, :2], bits(new)[0, :, 3:])
+        assert torch.equal(got[0, :, 2:7], bits(new)[1])
+    c.lens.copy_(i32([13, 2], dev))
+    c.accept(i32([[1, 4], [0, 3]], dev))
+    assert pbs.device_status() == 0 and c.lens.tolist() == [15, 4]
+    assert torch.equal(bits(c.k)[0, 3, :, 13:15], bits(new)[0, :, [1, 4]])
+
+
 @pytest.mark.parametrize("lead", [(), (2,)])
 def test_append_refuses_rows_inside_the_pools(lead, dev):
     """k or v cut out of a pool, pools that share pages, and tables there; a
