@@ -454,8 +454,8 @@ typedef enum { PBS_BF16 = 0, PBS_FP16 = 1, PBS_FP32 = 2 } pbs_dtype;
  * element is rounded once.
  *
  *   q, q_out  [batch, hq, n, d]  (layer stride unused); q_out may be q and
- *             k_out k, rows and all, and no output overlaps anything else:
- *             refused (slices of one buffer may interleave)
+ *             k_out k, rows and all; an output that overlaps anything else
+ *             is refused (slices of one buffer may interleave)
  *   k, k_out  [batch, hkv, n, d] or k.p == NULL with hkv == 0
  *   pos       int32, pos[b * pos_batch + i] (pos_batch 0: one row for all)
  *   inv_freq  [rot/2] fp64, radians per position
@@ -520,9 +520,10 @@ pbs_status pbs_cache_reserve(int32_t *table, int32_t *refs, const int32_t *lens,
 /*
  * pbs_cache_append - rows i < count[s] (all n when count is NULL) of k, v
  * [layers, seqs, hkv, n, d] written at tokens start[s] + i. The pages must
- * be reserved, k and v (by the memory that they span) lie outside the pools, and
- * the pools apart: refused. No other row of the pools is touched. Rows without a page, or with c.refs on a page that
- * several sequences hold, are reported and skipped.
+ * be reserved. k and v, by the memory that they span, lie outside the pools, and
+ * the pools apart: else refused. Rows without a page, or with c.refs on a page
+ * that several sequences hold, are reported and skipped. No other row of the
+ * pools is touched.
  */
 pbs_status pbs_cache_append(pbs_rows k, pbs_rows v, int n, void *k_pages, void *v_pages,
                             const int32_t *table, const int32_t *start, const int32_t *count,
@@ -572,10 +573,9 @@ pbs_status pbs_cache_compact(void *k_pages, void *v_pages, int32_t *table, int32
  * [seqs, n] ascends strictly from 0 on, so a draft only moves down; a
  * sequence whose path does not, or names a token that no page holds, is
  * reported and left alone.
- * The pools lie apart. The pages from token start[s] on must be the sequence's own
- * (reserved); with
- * c.refs a sequence whose accepted tokens come to lie in a page that several
- * hold is reported and left alone too.
+ * The pools lie apart. The pages from token start[s] on must be the sequence's
+ * own (reserved); with c.refs a sequence whose accepted tokens come to lie in a
+ * page that several hold is reported and left alone too.
  * lens (may be NULL): lens[s] = start[s] + count[s] where the path is good. It
  * may be start itself, or count (the lengths are then written by a second
  * kernel), and reaches into no other input.
@@ -615,8 +615,8 @@ pbs_status pbs_tree_mask(const int32_t *parents, uint32_t *mask, int32_t *depth,
  *        their lse too.
  * A token that a row does not see has no part in it, whatever its K and V
  * hold (NaN and infinities too). The workspace belongs to one call at a time:
- * calls that may overlap on the GPU need one each. out, lse and the workspace
- * overlap nothing: refused. The lengths, tables and masks may not change while
+ * calls that may overlap on the GPU need one each. An out, lse or workspace that
+ * overlaps anything else is refused. The lengths, tables and masks may not change while
  * the call runs.
  */
 pbs_status pbs_tree_attn(pbs_rows q, const void *k_pages, const void *v_pages,

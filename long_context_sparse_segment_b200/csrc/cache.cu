@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(256)
     x /= c.hkv;
     const int s = (int)(x % c.seqs), l = (int)(x / c.seqs);
     if (count && i >= count[s]) continue;
-    const int64_t o = token_word(table + (size_t)s * c.width, (int64_t)start[s] + i, c, words, true);
+    const int64_t o =
+        token_word(table + (size_t)s * c.width, (int64_t)start[s] + i, c, words, true);
     if (o < 0) {
       report(err, PBS_ERR_DEVICE_ASSERT);
       continue;
@@ -569,7 +570,8 @@ pbs_status pbs_cache_append(pbs_rows k, pbs_rows v, int n, void *k_pages, void *
     for (const pbs_rows &x : {k, v}) {
       const RowSet rows{x, c.seqs, c.hkv, n, c.d, 2};
       const int64_t up = 2 * x.layer * (c.layers - 1);  // bytes from the first layer to the last
-      meet |= bytes_meet(rows.low() + (up < 0 ? up : 0), rows.bytes() + (up < 0 ? -up : up), to, pool);
+      meet |= bytes_meet(rows.low() + (up < 0 ? up : 0), rows.bytes() + (up < 0 ? -up : up), to,
+                         pool);
     }
     meet |= bytes_meet(to, pool, table, each * c.width) || bytes_meet(to, pool, start, each) ||
             bytes_meet(to, pool, count, each) || bytes_meet(to, pool, c.refs, 4ll * c.pages);

@@ -531,7 +531,8 @@ cudaError_t launch_combine(const TreeArgs &a, int grid, cudaStream_t st) {
   // (four blocks an SM): 4 rows, with 4 threads a part, are 3 us quicker on one
   // sequence over 8192 tokens, 16 rows 14 us on 64 drafts of 8 sequences. Blocks
   // for four such rounds, then they walk the groups.
-  const int64_t rows = (int64_t)a.G * a.tree, heads = (int64_t)a.hkv * a.seqs, fit = 4 * sm_count_cached();
+  const int64_t rows = (int64_t)a.G * a.tree, heads = (int64_t)a.hkv * a.seqs;
+  const int64_t fit = 4 * sm_count_cached();
   const int rb = ceil_div(rows, 4) * heads <= fit ? 4 : 16;
   int64_t groups = ceil_div(rows, rb);
   // Where that is more than one round and the heads are twice the CTAs, a block
